@@ -258,6 +258,69 @@ int w4a8_prefill_linear_host(const float *x_host, const uint8_t *wq, const uint1
                              int64_t M, int64_t N, int64_t K, void *workspace,
                              size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Operators around the linears: a decoder layer's norm and gated activation with their output
+ * already in the 8-bit form that the next linear reads, and a linear whose weights are 8-bit
+ * floating point.  The conventions above hold (device pointers, stream, statuses, nothing
+ * allocated); none of these calls takes a workspace.
+ *
+ * A row's values are t[k], times a factor r that is common to the row:
+ *   rmsnorm   h = x + residual (fp32; just x without a residual), t = h * gamma,
+ *             r = 1 / sqrt(mean_k h^2 + eps)
+ *   swiglu    t = gate / (1 + exp(-gate)) * up, r = 1
+ *   quant     t = x, r = 1
+ * The quantizers divide by a multiple of the largest magnitude, so r only enters the scales:
+ *   INT8      s = max_k |t| / 127, a_q = clamp(round_half_away(t / s), +-127) (0 where s = 0),
+ *             a_scale[m] = s * r, rowsum[m][b] = sum of the 64 codes of block b: the arrays that
+ *             w4a8_linear takes.  K must be a positive multiple of 64.
+ *   operand   the same codes, scales and sums as the opaque buffer of w4a8_prepare_activations
+ *             (w4a8_prepared_activations_bytes(M, K) bytes), which w4a8_linear_prepared and
+ *             w4a8_linear_act take.
+ *   e4m3      per 128 columns b with v = max |t|: a_q = e4m3(t * (448 / v)), round to nearest even,
+ *             a_scale[b][m] = v / 448 * r; 0 and 0 where v < 2^-100: the arrays that
+ *             w4a8_fp8_linear takes.  K must be a positive multiple of 16 (the last block may be
+ *             short); a_q has [M][K] bytes and a_scale [ceil(K/128)][M] floats.
+ * Up to the codes every step is one fp32 IEEE operation (swiglu: after t), so the codes of rmsnorm
+ * and quant are defined bit for bit; sums of squares are taken in fp32.
+ *   - in_dtype: the type of x, residual, residual_out, gate and up, W4A8_IN_F32 or W4A8_IN_BF16
+ *     (anything else: W4A8_ERR_ARG).  gamma is fp32 [K], eps finite and > 0 (W4A8_ERR_ARG).
+ *   - residual may be NULL; residual_out (the sum h rounded once to in_dtype) may be NULL, be
+ *     `residual` or x themselves (in place), and must be NULL where residual is.
+ *   - gate and up are [M][K] with rows `ld` elements apart (ld >= K; ld * element size a multiple
+ *     of 16 bytes, else W4A8_ERR_ALIGN): with ld = 2 K and up = gate + K the two halves of one
+ *     projection's output.  The other arrays have no padding.
+ *   - 16-byte alignment: x, residual, residual_out, gate, up, gamma, a_q, act.  4 bytes: a_scale,
+ *     rowsum. */
+#define W4A8_IN_F32 0
+#define W4A8_IN_BF16 1
+int w4a8_rmsnorm_quant(const void *x, const void *residual, const float *gamma, float eps, int in_dtype,
+                       void *residual_out, int8_t *a_q, float *a_scale, int32_t *rowsum,
+                       int64_t M, int64_t K, void *stream);
+int w4a8_rmsnorm_prepare(const void *x, const void *residual, const float *gamma, float eps, int in_dtype,
+                         void *residual_out, void *act, size_t act_bytes, int64_t M, int64_t K, void *stream);
+int w4a8_rmsnorm_quant_fp8(const void *x, const void *residual, const float *gamma, float eps, int in_dtype,
+                           void *residual_out, uint8_t *a_q, float *a_scale, int64_t M, int64_t K,
+                           void *stream);
+int w4a8_swiglu_quant(const void *gate, const void *up, int64_t ld, int in_dtype, int8_t *a_q, float *a_scale,
+                      int32_t *rowsum, int64_t M, int64_t K, void *stream);
+int w4a8_swiglu_prepare(const void *gate, const void *up, int64_t ld, int in_dtype, void *act, size_t act_bytes,
+                        int64_t M, int64_t K, void *stream);
+int w4a8_swiglu_quant_fp8(const void *gate, const void *up, int64_t ld, int in_dtype, uint8_t *a_q,
+                          float *a_scale, int64_t M, int64_t K, void *stream);
+int w4a8_quant_fp8(const void *x, int in_dtype, uint8_t *a_q, float *a_scale, int64_t M, int64_t K, void *stream);
+
+/* Linear with e4m3 operands and a scale for each block of 128:
+ *   y[m,n] = sum_b a_scale[b,m] * w_scale[n / 128, b] * sum_{k in block b} a_q[m,k] * w_q[n,k] + bias[n]
+ * a_q e4m3 [M][K], a_scale fp32 [ceil(K/128)][M] (what the calls above write), w_q e4m3 [N][K],
+ * w_scale fp32 [ceil(N/128)][ceil(K/128)] (one per 128 x 128 weights), bias fp32 [N] or NULL;
+ * y [M][N] of out_dtype W4A8_OUT_F32 or W4A8_OUT_BF16 (anything else: W4A8_ERR_ARG).  K must be a
+ * positive multiple of 16; M and N are any sizes.  Inside a block the tensor cores sum in fp32;
+ * the blocks are summed in fp32 in an order that depends only on (M, N, K) and the GPU's SM
+ * count, so equal calls give equal bits.  A NaN code (0x7f, 0xff) makes its outputs NaN.
+ * 16-byte alignment: a_q, w_q, y; 4 bytes: a_scale, w_scale, bias. */
+int w4a8_fp8_linear(const uint8_t *a_q, const float *a_scale, const uint8_t *w_q, const float *w_scale,
+                    const float *bias, void *y, int out_dtype, int64_t M, int64_t N, int64_t K, void *stream);
+
 /* Workspace sizes in bytes (0 for an empty problem; (size_t)-1 for invalid shapes). */
 size_t w4a8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 size_t w4a8_prefill_workspace_bytes(int64_t M, int64_t N, int64_t K);

@@ -28,6 +28,7 @@ NOALLOC_SCRATCH_BYTES = 16 << 20
 OUT_F32 = 0
 OUT_BF16 = 1
 _OUT_DTYPES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+_IN_DTYPES = {torch.float32: 0, torch.bfloat16: 1}   # W4A8_IN_F32, W4A8_IN_BF16
 
 # name -> (restype, argtypes); every symbol include/w4a8.h declares
 _P = ctypes.c_void_p
@@ -58,6 +59,14 @@ SIGNATURES = {
     "w4a8_prefill_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "w4a8_debug_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "w4a8_debug_block_acc": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _SZ, _P]),
+    "w4a8_rmsnorm_quant": (ctypes.c_int, [_P, _P, _P, ctypes.c_float, ctypes.c_int, _P, _P, _P, _P, _I64, _I64, _P]),
+    "w4a8_rmsnorm_prepare": (ctypes.c_int, [_P, _P, _P, ctypes.c_float, ctypes.c_int, _P, _P, _SZ, _I64, _I64, _P]),
+    "w4a8_rmsnorm_quant_fp8": (ctypes.c_int, [_P, _P, _P, ctypes.c_float, ctypes.c_int, _P, _P, _P, _I64, _I64, _P]),
+    "w4a8_swiglu_quant": (ctypes.c_int, [_P, _P, _I64, ctypes.c_int, _P, _P, _P, _I64, _I64, _P]),
+    "w4a8_swiglu_prepare": (ctypes.c_int, [_P, _P, _I64, ctypes.c_int, _P, _SZ, _I64, _I64, _P]),
+    "w4a8_swiglu_quant_fp8": (ctypes.c_int, [_P, _P, _I64, ctypes.c_int, _P, _P, _I64, _I64, _P]),
+    "w4a8_quant_fp8": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _I64, _I64, _P]),
+    "w4a8_fp8_linear": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int, _I64, _I64, _I64, _P]),
     "w4a8_tape_begin": (ctypes.c_int, [_P]),
     "w4a8_tape_end": (ctypes.c_int, [_P, ctypes.POINTER(_P)]),
     "w4a8_tape_replay": (ctypes.c_int, [_P, _P]),
@@ -493,6 +502,180 @@ def linear_act(act, wq, w_scale, w_zero, M: int, N: int, K: int, bias=None, y=No
     rc = load().w4a8_linear_act(_ptr(act), _ptr(wq), _ptr(w_scale), _ptr(w_zero), _ptr(bias), _ptr(y), M, N, K,
                                 _ptr(ws), _nbytes(ws), _stream(stream))
     _check(rc, "w4a8_linear_act")
+    return y
+
+
+# ---------------------------------------------------------------- operators around the linears
+def _rows_in(x, name: str):
+    """Shape (M, K), input type code and device of a row operator's 2-D contiguous input."""
+    _want(x, None, name)
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D [M, K], got shape {tuple(x.shape)}")
+    if x.dtype not in _IN_DTYPES:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {x.dtype}")
+    return x.shape[0], x.shape[1], _IN_DTYPES[x.dtype], x.device
+
+
+def _norm_in(x, weight, residual, residual_out):
+    M, K, code, dev = _rows_in(x, "x")
+    _arg(weight, torch.float32, (K,), "weight", dev)
+    if weight is None:
+        raise TypeError("weight must be a torch.Tensor, got None")
+    _arg(residual, x.dtype, (M, K), "residual", dev)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+    elif residual_out is None:
+        residual_out = torch.empty_like(residual)
+    else:
+        _arg(residual_out, x.dtype, (M, K), "residual_out", dev)
+    return M, K, code, dev, residual_out
+
+
+def _gate_up(gate, up):
+    """Two [M, K] tensors with unit column stride and one row stride (gate's), e.g. the halves of
+    one projection's output."""
+    for t, name in ((gate, "gate"), (up, "up")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path), got {t.device}")
+    if gate.dtype not in _IN_DTYPES:
+        raise TypeError(f"gate must be torch.float32 or torch.bfloat16, got {gate.dtype}")
+    if up.dtype != gate.dtype:
+        raise TypeError(f"up must be {gate.dtype}, got {up.dtype}")
+    if gate.dim() != 2 or up.shape != gate.shape:
+        raise ValueError(f"gate and up must be 2-D of one shape, got {tuple(gate.shape)} and {tuple(up.shape)}")
+    M, K = gate.shape
+    ld = gate.stride(0) if M > 1 else K
+    if M and K and (gate.stride(1) != 1 or up.stride(1) != 1 or (M > 1 and up.stride(0) != ld) or ld < K):
+        raise ValueError(f"gate and up must have unit column stride and one row stride, got strides "
+                         f"{gate.stride()} and {up.stride()}")
+    if up.device != gate.device:
+        raise ValueError(f"up is on {up.device}, the call's other tensors on {gate.device}")
+    if gate.device.index != torch.cuda.current_device():
+        raise ValueError(f"gate is on {gate.device} but the current CUDA device is "
+                         f"{torch.cuda.current_device()} (the library runs on the current device)")
+    return M, K, max(ld, K), _IN_DTYPES[gate.dtype], gate.device
+
+
+def _int8_out(M, K, dev, a_q, a_scale, rowsum):
+    a_q = torch.empty((M, K), dtype=torch.int8, device=dev) if a_q is None else a_q
+    a_scale = torch.empty((M,), dtype=torch.float32, device=dev) if a_scale is None else a_scale
+    rowsum = torch.empty((M, K // 64), dtype=torch.int32, device=dev) if rowsum is None else rowsum
+    _arg(a_q, torch.int8, (M, K), "a_q", dev)
+    _arg(a_scale, torch.float32, (M,), "a_scale", dev)
+    _arg(rowsum, torch.int32, (M, K // 64), "rowsum", dev)
+    return a_q, a_scale, rowsum
+
+
+def _e4m3_out(M, K, dev, a_q, a_scale):
+    nb = (K + 127) // 128
+    a_q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev) if a_q is None else a_q
+    a_scale = torch.empty((nb, M), dtype=torch.float32, device=dev) if a_scale is None else a_scale
+    _arg(a_q, torch.float8_e4m3fn, (M, K), "a_q", dev)
+    _arg(a_scale, torch.float32, (nb, M), "a_scale", dev)
+    return a_q, a_scale
+
+
+def _act_out(M, K, dev, act):
+    act = workspace(prepared_activations_bytes(M, K), dev) if act is None else act
+    _arg(act, None, None, "act", dev)
+    return act
+
+
+def rmsnorm_quant(x, weight, eps, residual=None, residual_out=None, a_q=None, a_scale=None, rowsum=None, stream=None):
+    """w4a8_rmsnorm_quant: rms_norm(x + residual) * weight as INT8 codes for `linear`.  Returns
+    (a_q int8 [M,K], a_scale fp32 [M], rowsum int32 [M,K/64], x + residual or None)."""
+    M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out)
+    a_q, a_scale, rowsum = _int8_out(M, K, dev, a_q, a_scale, rowsum)
+    rc = load().w4a8_rmsnorm_quant(_ptr(x), _ptr(residual), _ptr(weight), float(eps), code, _ptr(residual_out),
+                                   _ptr(a_q), _ptr(a_scale), _ptr(rowsum), M, K, _stream(stream))
+    _check(rc, "w4a8_rmsnorm_quant")
+    return a_q, a_scale, rowsum, residual_out
+
+
+def rmsnorm_prepare(x, weight, eps, residual=None, residual_out=None, act=None, stream=None):
+    """w4a8_rmsnorm_prepare: rms_norm(x + residual) * weight as the opaque operand of
+    `linear_prepared` and `linear_act`.  Returns (act, x + residual or None)."""
+    M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out)
+    act = _act_out(M, K, dev, act)
+    rc = load().w4a8_rmsnorm_prepare(_ptr(x), _ptr(residual), _ptr(weight), float(eps), code, _ptr(residual_out),
+                                     _ptr(act), _nbytes(act), M, K, _stream(stream))
+    _check(rc, "w4a8_rmsnorm_prepare")
+    return act, residual_out
+
+
+def rmsnorm_quant_fp8(x, weight, eps, residual=None, residual_out=None, a_q=None, a_scale=None, stream=None):
+    """w4a8_rmsnorm_quant_fp8: rms_norm(x + residual) * weight as e4m3 codes for `fp8_linear`.
+    Returns (a_q e4m3 [M,K], a_scale fp32 [ceil(K/128),M], x + residual or None)."""
+    M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out)
+    a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
+    rc = load().w4a8_rmsnorm_quant_fp8(_ptr(x), _ptr(residual), _ptr(weight), float(eps), code, _ptr(residual_out),
+                                       _ptr(a_q), _ptr(a_scale), M, K, _stream(stream))
+    _check(rc, "w4a8_rmsnorm_quant_fp8")
+    return a_q, a_scale, residual_out
+
+
+def swiglu_quant(gate, up, a_q=None, a_scale=None, rowsum=None, stream=None):
+    """w4a8_swiglu_quant: silu(gate) * up as INT8 codes for `linear`.  Returns (a_q, a_scale, rowsum)."""
+    M, K, ld, code, dev = _gate_up(gate, up)
+    a_q, a_scale, rowsum = _int8_out(M, K, dev, a_q, a_scale, rowsum)
+    rc = load().w4a8_swiglu_quant(_ptr(gate), _ptr(up), ld, code, _ptr(a_q), _ptr(a_scale), _ptr(rowsum), M, K,
+                                  _stream(stream))
+    _check(rc, "w4a8_swiglu_quant")
+    return a_q, a_scale, rowsum
+
+
+def swiglu_prepare(gate, up, act=None, stream=None):
+    """w4a8_swiglu_prepare: silu(gate) * up as the opaque operand of `linear_prepared` and
+    `linear_act` (returned)."""
+    M, K, ld, code, dev = _gate_up(gate, up)
+    act = _act_out(M, K, dev, act)
+    rc = load().w4a8_swiglu_prepare(_ptr(gate), _ptr(up), ld, code, _ptr(act), _nbytes(act), M, K, _stream(stream))
+    _check(rc, "w4a8_swiglu_prepare")
+    return act
+
+
+def swiglu_quant_fp8(gate, up, a_q=None, a_scale=None, stream=None):
+    """w4a8_swiglu_quant_fp8: silu(gate) * up as e4m3 codes for `fp8_linear`.  Returns
+    (a_q e4m3 [M,K], a_scale fp32 [ceil(K/128),M])."""
+    M, K, ld, code, dev = _gate_up(gate, up)
+    a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
+    rc = load().w4a8_swiglu_quant_fp8(_ptr(gate), _ptr(up), ld, code, _ptr(a_q), _ptr(a_scale), M, K, _stream(stream))
+    _check(rc, "w4a8_swiglu_quant_fp8")
+    return a_q, a_scale
+
+
+def quant_fp8(x, a_q=None, a_scale=None, stream=None):
+    """w4a8_quant_fp8: x as e4m3 codes for `fp8_linear`.  Returns (a_q, a_scale)."""
+    M, K, code, dev = _rows_in(x, "x")
+    a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
+    rc = load().w4a8_quant_fp8(_ptr(x), code, _ptr(a_q), _ptr(a_scale), M, K, _stream(stream))
+    _check(rc, "w4a8_quant_fp8")
+    return a_q, a_scale
+
+
+def fp8_linear(a_q, a_scale, w_q, w_scale, bias=None, y=None, out_dtype=None, stream=None):
+    """w4a8_fp8_linear: e4m3 activations [M,K] with a_scale fp32 [ceil(K/128),M], e4m3 weights
+    [N,K] with w_scale fp32 [ceil(N/128),ceil(K/128)] -> y fp32 or bf16 [M,N]."""
+    _want(a_q, torch.float8_e4m3fn, "a_q")
+    _want(w_q, torch.float8_e4m3fn, "w_q")
+    if a_q.dim() != 2 or w_q.dim() != 2:
+        raise ValueError(f"a_q and w_q must be 2-D, got shapes {tuple(a_q.shape)} and {tuple(w_q.shape)}")
+    M, K = a_q.shape
+    N = w_q.shape[0]
+    dev, nb = a_q.device, (K + 127) // 128
+    _arg(w_q, torch.float8_e4m3fn, (N, K), "w_q", dev)
+    _arg(a_scale, torch.float32, (nb, M), "a_scale", dev)
+    _arg(w_scale, torch.float32, ((N + 127) // 128, nb), "w_scale", dev)
+    if a_scale is None or w_scale is None:
+        raise TypeError("a_scale and w_scale must be torch.Tensors")
+    _arg(bias, torch.float32, (N,), "bias", dev)
+    y, code = _out(y, (M, N), dev, out_dtype if y is None else y.dtype)
+    rc = load().w4a8_fp8_linear(_ptr(a_q), _ptr(a_scale), _ptr(w_q), _ptr(w_scale), _ptr(bias), _ptr(y), code,
+                                M, N, K, _stream(stream))
+    _check(rc, "w4a8_fp8_linear")
     return y
 
 

@@ -2,6 +2,7 @@
 // carving, routing by shape and kernel launches.  Nothing here allocates memory; the
 // host-buffer call keeps a few streams and events per device, created on first use.
 #include "../../include/w4a8.h"
+#include "ops_internal.h"
 #include "w4a8_internal.h"
 
 #include <algorithm>
@@ -234,6 +235,16 @@ int linear_prepared_impl(const void* act, const void* pw, const float* bias, con
                          int64_t N, int64_t K, void* stream);
 
 }  // namespace
+
+int device_info(int* num_sms, uint32_t** status) {
+    DeviceInfo* d = nullptr;
+    const int rc = current_device(&d);
+    if (rc != W4A8_OK) return rc;
+    *num_sms = d->num_sms;
+    *status = d->status;
+    return W4A8_OK;
+}
+
 }  // namespace w4a8
 
 using namespace w4a8;
