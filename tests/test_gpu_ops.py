@@ -252,7 +252,7 @@ SHAPES = [(1, 1, 16), (1, 64, 128), (1, 1024, 1024), (2, 130, 144), (8, 3072, 10
           (17, 1000, 1040), (31, 129, 4096), (33, 640, 640), (63, 384, 896), (64, 2048, 6144), (65, 1001, 1040),
           (127, 127, 272), (128, 128, 128), (129, 255, 400), (200, 512, 512), (256, 256, 256), (257, 770, 1040),
           (512, 1024, 2048), (513, 3073, 656), (777, 1001, 1040), (1024, 2048, 1024), (1500, 1111, 272),
-          (2050, 4100, 528), (1, 14336, 4096), (4, 4096, 14336)]
+          (2050, 4100, 528), (4097, 2571, 1040), (2600, 4104, 16), (1, 14336, 4096), (4, 4096, 14336)]
 
 
 @pytest.mark.parametrize("dt", [BF, F32])

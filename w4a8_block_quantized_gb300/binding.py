@@ -506,6 +506,32 @@ def linear_act(act, wq, w_scale, w_zero, M: int, N: int, K: int, bias=None, y=No
 
 
 # ---------------------------------------------------------------- operators around the linears
+# These calls are short on the GPU (a few microseconds for a token), so what Python does around
+# the library call counts.  Each checks its tensors with `_fits`, a pass over cheap attributes
+# that allocates nothing, and goes through the checks that name the offending argument only where
+# that fails; addresses are passed as plain integers; and the current stream is taken as a raw
+# handle.  Measured on the GPU's host, one token through rmsnorm_quant: 13.7 -> 6.2 us a call (the
+# library call itself 2.6; a stream object alone costs 2.8, the raw handle 0.08).
+def _handle(index: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _fits(index: int, *args) -> bool:
+    """Whether every (tensor, dtype, shape) is a contiguous CUDA tensor of that dtype and shape on
+    device `index`, the current device."""
+    try:
+        for t, dtype, shape in args:
+            if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+                return False
+    except AttributeError:
+        return False
+    return index == torch.cuda.current_device()
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _rows_in(x, name: str):
     """Shape (M, K), input type code and device of a row operator's 2-D contiguous input."""
     _want(x, None, name)
@@ -533,8 +559,8 @@ def _norm_in(x, weight, residual, residual_out):
 
 
 def _gate_up(gate, up):
-    """Two [M, K] tensors with unit column stride and one row stride (gate's), e.g. the halves of
-    one projection's output."""
+    """(M, K, row stride, input type code, device) of two [M, K] tensors with unit column stride and
+    one row stride, e.g. the halves of one projection's output."""
     for t, name in ((gate, "gate"), (up, "up")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
@@ -542,30 +568,33 @@ def _gate_up(gate, up):
             raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path), got {t.device}")
     if gate.dtype not in _IN_DTYPES:
         raise TypeError(f"gate must be torch.float32 or torch.bfloat16, got {gate.dtype}")
-    if up.dtype != gate.dtype:
+    if up.dtype is not gate.dtype:
         raise TypeError(f"up must be {gate.dtype}, got {up.dtype}")
     if gate.dim() != 2 or up.shape != gate.shape:
         raise ValueError(f"gate and up must be 2-D of one shape, got {tuple(gate.shape)} and {tuple(up.shape)}")
     M, K = gate.shape
-    ld = gate.stride(0) if M > 1 else K
-    if M and K and (gate.stride(1) != 1 or up.stride(1) != 1 or (M > 1 and up.stride(0) != ld) or ld < K):
+    (ld, one), (ldu, oneu) = gate.stride(), up.stride()
+    if M and K and (one != 1 or oneu != 1 or (M > 1 and (ldu != ld or ld < K))):
         raise ValueError(f"gate and up must have unit column stride and one row stride, got strides "
                          f"{gate.stride()} and {up.stride()}")
-    if up.device != gate.device:
+    dev = gate.get_device()
+    if up.get_device() != dev:
         raise ValueError(f"up is on {up.device}, the call's other tensors on {gate.device}")
-    if gate.device.index != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         raise ValueError(f"gate is on {gate.device} but the current CUDA device is "
                          f"{torch.cuda.current_device()} (the library runs on the current device)")
-    return M, K, max(ld, K), _IN_DTYPES[gate.dtype], gate.device
+    return M, K, (ld if M > 1 else K), _IN_DTYPES[gate.dtype], gate.device
 
 
 def _int8_out(M, K, dev, a_q, a_scale, rowsum):
     a_q = torch.empty((M, K), dtype=torch.int8, device=dev) if a_q is None else a_q
     a_scale = torch.empty((M,), dtype=torch.float32, device=dev) if a_scale is None else a_scale
     rowsum = torch.empty((M, K // 64), dtype=torch.int32, device=dev) if rowsum is None else rowsum
-    _arg(a_q, torch.int8, (M, K), "a_q", dev)
-    _arg(a_scale, torch.float32, (M,), "a_scale", dev)
-    _arg(rowsum, torch.int32, (M, K // 64), "rowsum", dev)
+    if not _fits(dev.index, (a_q, torch.int8, (M, K)), (a_scale, torch.float32, (M,)),
+                 (rowsum, torch.int32, (M, K // 64))):
+        _arg(a_q, torch.int8, (M, K), "a_q", dev)
+        _arg(a_scale, torch.float32, (M,), "a_scale", dev)
+        _arg(rowsum, torch.int32, (M, K // 64), "rowsum", dev)
     return a_q, a_scale, rowsum
 
 
@@ -573,8 +602,9 @@ def _e4m3_out(M, K, dev, a_q, a_scale):
     nb = (K + 127) // 128
     a_q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev) if a_q is None else a_q
     a_scale = torch.empty((nb, M), dtype=torch.float32, device=dev) if a_scale is None else a_scale
-    _arg(a_q, torch.float8_e4m3fn, (M, K), "a_q", dev)
-    _arg(a_scale, torch.float32, (nb, M), "a_scale", dev)
+    if not _fits(dev.index, (a_q, torch.float8_e4m3fn, (M, K)), (a_scale, torch.float32, (nb, M))):
+        _arg(a_q, torch.float8_e4m3fn, (M, K), "a_q", dev)
+        _arg(a_scale, torch.float32, (nb, M), "a_scale", dev)
     return a_q, a_scale
 
 
@@ -584,13 +614,29 @@ def _act_out(M, K, dev, act):
     return act
 
 
+def _norm(x, weight, residual, residual_out):
+    """_norm_in with the common case (every tensor given and fitting) checked in one pass."""
+    if residual is not None and residual_out is not None:
+        try:
+            dt, shape = x.dtype, x.shape
+            M, K = shape
+            code = _IN_DTYPES[dt]
+            if _fits(x.get_device(), (x, dt, shape), (weight, torch.float32, (K,)), (residual, dt, shape),
+                     (residual_out, dt, shape)):
+                return M, K, code, x.device, residual_out
+        except (AttributeError, KeyError, ValueError):
+            pass
+    return _norm_in(x, weight, residual, residual_out)
+
+
 def rmsnorm_quant(x, weight, eps, residual=None, residual_out=None, a_q=None, a_scale=None, rowsum=None, stream=None):
     """w4a8_rmsnorm_quant: rms_norm(x + residual) * weight as INT8 codes for `linear`.  Returns
     (a_q int8 [M,K], a_scale fp32 [M], rowsum int32 [M,K/64], x + residual or None)."""
-    M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out)
+    M, K, code, dev, residual_out = _norm(x, weight, residual, residual_out)
     a_q, a_scale, rowsum = _int8_out(M, K, dev, a_q, a_scale, rowsum)
-    rc = load().w4a8_rmsnorm_quant(_ptr(x), _ptr(residual), _ptr(weight), float(eps), code, _ptr(residual_out),
-                                   _ptr(a_q), _ptr(a_scale), _ptr(rowsum), M, K, _stream(stream))
+    rc = load().w4a8_rmsnorm_quant(x.data_ptr(), _adr(residual), weight.data_ptr(), eps, code, _adr(residual_out),
+                                   a_q.data_ptr(), a_scale.data_ptr(), rowsum.data_ptr(), M, K,
+                                   _handle(dev.index, stream))
     _check(rc, "w4a8_rmsnorm_quant")
     return a_q, a_scale, rowsum, residual_out
 
@@ -598,10 +644,10 @@ def rmsnorm_quant(x, weight, eps, residual=None, residual_out=None, a_q=None, a_
 def rmsnorm_prepare(x, weight, eps, residual=None, residual_out=None, act=None, stream=None):
     """w4a8_rmsnorm_prepare: rms_norm(x + residual) * weight as the opaque operand of
     `linear_prepared` and `linear_act`.  Returns (act, x + residual or None)."""
-    M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out)
+    M, K, code, dev, residual_out = _norm(x, weight, residual, residual_out)
     act = _act_out(M, K, dev, act)
-    rc = load().w4a8_rmsnorm_prepare(_ptr(x), _ptr(residual), _ptr(weight), float(eps), code, _ptr(residual_out),
-                                     _ptr(act), _nbytes(act), M, K, _stream(stream))
+    rc = load().w4a8_rmsnorm_prepare(x.data_ptr(), _adr(residual), weight.data_ptr(), eps, code, _adr(residual_out),
+                                     act.data_ptr(), _nbytes(act), M, K, _handle(dev.index, stream))
     _check(rc, "w4a8_rmsnorm_prepare")
     return act, residual_out
 
@@ -609,10 +655,10 @@ def rmsnorm_prepare(x, weight, eps, residual=None, residual_out=None, act=None, 
 def rmsnorm_quant_fp8(x, weight, eps, residual=None, residual_out=None, a_q=None, a_scale=None, stream=None):
     """w4a8_rmsnorm_quant_fp8: rms_norm(x + residual) * weight as e4m3 codes for `fp8_linear`.
     Returns (a_q e4m3 [M,K], a_scale fp32 [ceil(K/128),M], x + residual or None)."""
-    M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out)
+    M, K, code, dev, residual_out = _norm(x, weight, residual, residual_out)
     a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
-    rc = load().w4a8_rmsnorm_quant_fp8(_ptr(x), _ptr(residual), _ptr(weight), float(eps), code, _ptr(residual_out),
-                                       _ptr(a_q), _ptr(a_scale), M, K, _stream(stream))
+    rc = load().w4a8_rmsnorm_quant_fp8(x.data_ptr(), _adr(residual), weight.data_ptr(), eps, code, _adr(residual_out),
+                                       a_q.data_ptr(), a_scale.data_ptr(), M, K, _handle(dev.index, stream))
     _check(rc, "w4a8_rmsnorm_quant_fp8")
     return a_q, a_scale, residual_out
 
@@ -621,8 +667,8 @@ def swiglu_quant(gate, up, a_q=None, a_scale=None, rowsum=None, stream=None):
     """w4a8_swiglu_quant: silu(gate) * up as INT8 codes for `linear`.  Returns (a_q, a_scale, rowsum)."""
     M, K, ld, code, dev = _gate_up(gate, up)
     a_q, a_scale, rowsum = _int8_out(M, K, dev, a_q, a_scale, rowsum)
-    rc = load().w4a8_swiglu_quant(_ptr(gate), _ptr(up), ld, code, _ptr(a_q), _ptr(a_scale), _ptr(rowsum), M, K,
-                                  _stream(stream))
+    rc = load().w4a8_swiglu_quant(gate.data_ptr(), up.data_ptr(), ld, code, a_q.data_ptr(), a_scale.data_ptr(),
+                                  rowsum.data_ptr(), M, K, _handle(dev.index, stream))
     _check(rc, "w4a8_swiglu_quant")
     return a_q, a_scale, rowsum
 
@@ -632,7 +678,8 @@ def swiglu_prepare(gate, up, act=None, stream=None):
     `linear_act` (returned)."""
     M, K, ld, code, dev = _gate_up(gate, up)
     act = _act_out(M, K, dev, act)
-    rc = load().w4a8_swiglu_prepare(_ptr(gate), _ptr(up), ld, code, _ptr(act), _nbytes(act), M, K, _stream(stream))
+    rc = load().w4a8_swiglu_prepare(gate.data_ptr(), up.data_ptr(), ld, code, act.data_ptr(), _nbytes(act), M, K,
+                                    _handle(dev.index, stream))
     _check(rc, "w4a8_swiglu_prepare")
     return act
 
@@ -642,7 +689,8 @@ def swiglu_quant_fp8(gate, up, a_q=None, a_scale=None, stream=None):
     (a_q e4m3 [M,K], a_scale fp32 [ceil(K/128),M])."""
     M, K, ld, code, dev = _gate_up(gate, up)
     a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
-    rc = load().w4a8_swiglu_quant_fp8(_ptr(gate), _ptr(up), ld, code, _ptr(a_q), _ptr(a_scale), M, K, _stream(stream))
+    rc = load().w4a8_swiglu_quant_fp8(gate.data_ptr(), up.data_ptr(), ld, code, a_q.data_ptr(), a_scale.data_ptr(),
+                                      M, K, _handle(dev.index, stream))
     _check(rc, "w4a8_swiglu_quant_fp8")
     return a_q, a_scale
 
@@ -651,14 +699,14 @@ def quant_fp8(x, a_q=None, a_scale=None, stream=None):
     """w4a8_quant_fp8: x as e4m3 codes for `fp8_linear`.  Returns (a_q, a_scale)."""
     M, K, code, dev = _rows_in(x, "x")
     a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
-    rc = load().w4a8_quant_fp8(_ptr(x), code, _ptr(a_q), _ptr(a_scale), M, K, _stream(stream))
+    rc = load().w4a8_quant_fp8(x.data_ptr(), code, a_q.data_ptr(), a_scale.data_ptr(), M, K,
+                               _handle(dev.index, stream))
     _check(rc, "w4a8_quant_fp8")
     return a_q, a_scale
 
 
-def fp8_linear(a_q, a_scale, w_q, w_scale, bias=None, y=None, out_dtype=None, stream=None):
-    """w4a8_fp8_linear: e4m3 activations [M,K] with a_scale fp32 [ceil(K/128),M], e4m3 weights
-    [N,K] with w_scale fp32 [ceil(N/128),ceil(K/128)] -> y fp32 or bf16 [M,N]."""
+def _fp8_in(a_q, a_scale, w_q, w_scale, bias, y, out_dtype):
+    """The checks of fp8_linear that name the offending argument; y allocated when absent."""
     _want(a_q, torch.float8_e4m3fn, "a_q")
     _want(w_q, torch.float8_e4m3fn, "w_q")
     if a_q.dim() != 2 or w_q.dim() != 2:
@@ -672,9 +720,29 @@ def fp8_linear(a_q, a_scale, w_q, w_scale, bias=None, y=None, out_dtype=None, st
     if a_scale is None or w_scale is None:
         raise TypeError("a_scale and w_scale must be torch.Tensors")
     _arg(bias, torch.float32, (N,), "bias", dev)
-    y, code = _out(y, (M, N), dev, out_dtype if y is None else y.dtype)
-    rc = load().w4a8_fp8_linear(_ptr(a_q), _ptr(a_scale), _ptr(w_q), _ptr(w_scale), _ptr(bias), _ptr(y), code,
-                                M, N, K, _stream(stream))
+    y, _ = _out(y, (M, N), dev, out_dtype if y is None else y.dtype)
+    return M, N, K, y
+
+
+def fp8_linear(a_q, a_scale, w_q, w_scale, bias=None, y=None, out_dtype=None, stream=None):
+    """w4a8_fp8_linear: e4m3 activations [M,K] with a_scale fp32 [ceil(K/128),M], e4m3 weights
+    [N,K] with w_scale fp32 [ceil(N/128),ceil(K/128)] -> y fp32 or bf16 [M,N]."""
+    fits = False
+    if y is not None:
+        try:
+            e8, f32 = torch.float8_e4m3fn, torch.float32
+            (M, K), (N, _) = a_q.shape, w_q.shape
+            nb, dev = (K + 127) // 128, a_q.get_device()
+            args = (a_q, e8, (M, K)), (a_scale, f32, (nb, M)), (w_q, e8, (N, K)), (w_scale, f32, ((N + 127) // 128, nb))
+            fits = y.dtype in _OUT_DTYPES and _fits(dev, *args, (y, y.dtype, (M, N))) and \
+                (bias is None or _fits(dev, (bias, f32, (N,))))
+        except (AttributeError, ValueError):
+            fits = False
+    if not fits:
+        M, N, K, y = _fp8_in(a_q, a_scale, w_q, w_scale, bias, y, out_dtype)
+        dev = y.get_device()
+    rc = load().w4a8_fp8_linear(a_q.data_ptr(), a_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), _adr(bias),
+                                y.data_ptr(), _OUT_DTYPES[y.dtype], M, N, K, _handle(dev, stream))
     _check(rc, "w4a8_fp8_linear")
     return y
 

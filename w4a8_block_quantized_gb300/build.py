@@ -46,11 +46,12 @@ def up_to_date() -> bool:
 
 
 # Kernels that re-split registers between warpgroups (setmaxnreg) need exactly this many
-# registers per thread at launch: the split in gemm.cu is sized against it, and a smaller
+# registers per thread at launch: the splits in gemm.cu and fp8_gemm.cu are sized against it, and a smaller
 # launch allocation would leave setmaxnreg.inc waiting for registers that never come.  Keys
 # are matched against the mangled entry names; the debug instantiation of the 256-token
 # kernel (template argument true, "ILb1E") does not re-split and is not checked.
-REGISTER_SPLIT_KERNELS = {"gemm_kernel": 96, "gemm_wide_kernelILb0E": 96, "gemm_packed_kernel": 96}
+REGISTER_SPLIT_KERNELS = {"11gemm_kernel": 96, "gemm_wide_kernelILb0E": 96, "gemm_packed_kernel": 96,
+                          "fp8_pair_kernel": 96}
 
 
 def check_register_split(ptxas_log: str) -> None:
@@ -87,7 +88,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        split = os.path.basename(src) == "gemm.cu"
+        split = os.path.basename(src) in ("gemm.cu", "fp8_gemm.cu")
         cmd = [cc, *common, *([] if ptxas_verbose or not split else ["-Xptxas", "-v"]), "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
