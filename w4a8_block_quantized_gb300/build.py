@@ -51,7 +51,7 @@ def up_to_date() -> bool:
 # are matched against the mangled entry names; the debug instantiation of the 256-token
 # kernel (template argument true, "ILb1E") does not re-split and is not checked.
 REGISTER_SPLIT_KERNELS = {"11gemm_kernel": 96, "gemm_wide_kernelILb0E": 96, "gemm_packed_kernel": 96,
-                          "fp8_pair_kernel": 96}
+                          "fp8_pair_kernel": 96, "fp8_tok_kernelILi128E": 96}
 
 
 def check_register_split(ptxas_log: str) -> None:

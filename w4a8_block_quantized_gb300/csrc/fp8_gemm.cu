@@ -21,7 +21,10 @@ namespace w4a8 {
 namespace {
 
 constexpr uint32_t kLayoutSw128 = 2;
-constexpr int kThreads = 256;
+// Register split of the 640-thread kernels: launch = 640 x 96 (checked at build time); the first four
+// warps drop to 32, the sixteen draining warps rise to 112: 128 * 32 + 512 * 112 = 640 * 96.
+constexpr int kRegsLow = 32, kRegsHigh = 112, kSplitThreads = 640;
+static_assert(128 * kRegsLow + 512 * kRegsHigh == kSplitThreads * 96, "register split");
 
 struct Fp8Params {
     CUtensorMap amap, wmap, ymap;
@@ -32,6 +35,7 @@ struct Fp8Params {
     int bf16, vec;  // vec: 16-byte stores fit every row of y
     int64_t M, N;
     int nb, tiles_m, tiles_n;
+    int split;  // CTAs (a cluster) sharing a tile's K
     uint32_t* status;
     uint64_t wait_limit_ns;
 };
@@ -46,87 +50,167 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
     }
 }
 
-namespace base {
-constexpr int kBM = 128, kBN = 128, kStages = 4;
-constexpr int kATile = kBM * 128, kStageBytes = kATile + kBN * 128;
-constexpr int kOffBar = kStages * kStageBytes;
-constexpr int kSmemBytes = kOffBar + 256 + 1024;
-}  // namespace base
+// ---------------------------------------------------------------- one CTA, weights on the lanes
+// The form for few tokens and for problems that 256 x 256 tiles would not fill the GPU with.  Roles
+// are swapped: 128 weight rows are the MMA's M operand (TMEM lanes) and TN tokens its N operand, so
+// a tile is as narrow as the tokens ask for and a warp's stores run along a row of y.  A thread
+// owns one weight row; the factor sa sw then differs from column to column and comes from shared
+// memory, as products formed by a loader warp eight blocks at a time.
+//   warp 0      copies      warps 1-2  every other block's 4 MMAs      warp 3  factors
+//   warps 4..   drain, two sets: one takes the even blocks, one the odd
+// What bounds it: few tokens, the weights' stream from HBM (stages in flight, and K split over a
+// cluster of `split` CTAs so that every SM has some of it); more tokens, the drain.  Reading one
+// accumulator costs a warp about 700 cycles of waits in a row (barrier, factors, TMEM) however few
+// its columns, so the two sets work on two blocks at a time, each with sums of its own that are
+// added at the end of a tile (one set: 512 x 2048 -> 6144 took 27 us, now @@; 8 x 4096 -> 14336
+// 13.6 us, now @@).  A split sums each output's parts in the order of the ranks, each CTA for its
+// share of the columns, read from the others' shared memory.
+template <int TN_>
+struct Tok {
+    static constexpr int TN = TN_;
+    static constexpr int kSetWarps = TN <= 32 ? 4 : 8;  // warps of one set
+    static constexpr int kCols = TN * 4 / kSetWarps;    // columns a thread sums
+    static constexpr int kThreads = 128 + 64 * kSetWarps;
+    static constexpr int kNBuf = 4;                     // TMEM accumulators
+    static constexpr int kStages = TN <= 32 ? 10 : TN <= 64 ? 6 : 4;
+    static constexpr int kWBytes = 128 * 128, kStageBytes = kWBytes + TN * 128;
+    static constexpr uint32_t kTmemCols = TN * kNBuf;
+    static constexpr int kChunk = 8;                    // blocks per batch of factors
+    static constexpr int kOffPart = kStages * kStageBytes;  // the odd set's sums [column][weight row]
+    static constexpr int kOffScale = kOffPart + TN * 512;
+    static constexpr int kScaleBytes = kChunk * TN * 4;
+    static constexpr int kRawFloats = kChunk * TN + kChunk;  // the scales they are formed from: sa, then sw
+    static constexpr int kOffRaw = kOffScale + 2 * kScaleBytes;
+    static constexpr int kOffBar = kOffRaw + 2 * kRawFloats * 4;
+    static constexpr int kSmemBytes = kOffBar + 512 + 1024;
+    // Register split of the 640-thread form with 64 sums a thread (see the pair form).
+    static constexpr bool kResplit = kCols == 64;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+    static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 512, "TMEM allocation");
+    // Each stage and each accumulator has one issuer and one set at every phase (their counts are
+    // even); an accumulator's release for the block kNBuf later reaches that block's stage only
+    // after the stage's previous phase.
+    static_assert(kStages % 2 == 0 && kNBuf == 4 && kStages >= kNBuf, "phases");
+    static_assert(TN % 16 == 0 && kCols % 16 == 0, "MMA N; TMEM loads of 16 columns");
+};
 
-// Output columns n0 + 0 .. 31 of token m, with the bias where it is not in the sums already.
-template <bool BIAS>
-__device__ __forceinline__ void store_cols(const Fp8Params& p, int64_t m, int64_t n0, const float* y) {
-    if (m >= p.M) return;
-    if (p.vec && n0 + 32 <= p.N) {
-        if (p.bf16) {
-            uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + m * p.N + n0);
+// y[c] = fma(f[c], v[c], y[c]) for 16 columns, two per instruction; f from shared memory, the same
+// for every lane.
+__device__ __forceinline__ void fold16(float* y, const float* f, const uint32_t* v) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t u[4];
+    for (int c = 0; c < 16; c += 4) {
+        const ulonglong2 ff = *reinterpret_cast<const ulonglong2*>(f + c);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v0 = y[8 * i + 2 * e], v1 = y[8 * i + 2 * e + 1];
-                    if (BIAS && p.bias) v0 += p.bias[n0 + 8 * i + 2 * e], v1 += p.bias[n0 + 8 * i + 2 * e + 1];
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(v0, v1);
-                    u[e] = *reinterpret_cast<const uint32_t*>(&b);
-                }
-                d[i] = make_uint4(u[0], u[1], u[2], u[3]);
-            }
-        } else {
-            float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.y) + m * p.N + n0);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float4 v = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-                if (BIAS && p.bias) {
-                    const float* b = p.bias + n0 + 4 * i;
-                    v.x += b[0], v.y += b[1], v.z += b[2], v.w += b[3];
-                }
-                d[i] = v;
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const int64_t n = n0 + i;
-        if (n < p.N) {
-            const float v = BIAS && p.bias ? y[i] + p.bias[n] : y[i];
-            if (p.bf16) static_cast<__nv_bfloat16*>(p.y)[m * p.N + n] = __float2bfloat16_rn(v);
-            else static_cast<float*>(p.y)[m * p.N + n] = v;
+        for (int e = 0; e < 4; e += 2) {
+            uint64_t yy, vv;
+            asm("mov.b64 %0, {%1, %2};" : "=l"(yy) : "f"(y[c + e]), "f"(y[c + e + 1]));
+            asm("mov.b64 %0, {%1, %2};" : "=l"(vv) : "r"(v[c + e]), "r"(v[c + e + 1]));
+            asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(yy) : "l"(e ? ff.y : ff.x), "l"(vv));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(y[c + e]), "=f"(y[c + e + 1]) : "l"(yy));
         }
     }
 }
 
-// 128 x 128 output tiles, one CTA each in turn (persistent).  Warp 0 copies, warp 1 issues the
-// MMAs (4 of K = 32 a block), warps 4-7 drain: a thread holds its token's 128 sums.
-__global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
-    using namespace base;
+// The end of a tile: this thread's sums y of C columns (tokens m0 ..) of weight row n, of which it
+// keeps the half from column K0 on.  `part`: the tile's exchange area [column][weight row], at this
+// thread's first column and row; `threads`: of both sets.  Then the outputs, or, for a split tile, the
+// CTA's sums into the area.
+template <int C, int K0, int THREADS>
+__device__ __forceinline__ void finish_cols(const Fp8Params& p, float* part, const float (&y)[C], int64_t m0, int64_t n,
+                                            bool split, bool first) {
+    constexpr int G0 = C / 2 - K0;  // the half it hands over
+    if (!first) named_bar_sync(1, THREADS);  // the last tile's have been read
+#pragma unroll
+    for (int c = 0; c < C / 2; ++c) part[(G0 + c) * 128] = y[G0 + c];
+    named_bar_sync(1, THREADS);
+    if (split) {
+#pragma unroll
+        for (int c = 0; c < C / 2; ++c) part[(K0 + c) * 128] += y[K0 + c];
+        return;
+    }
+    if (n >= p.N) return;
+    const float bn = p.bias ? __ldcg(p.bias + n) : 0.0f;
+    const int live = p.M - m0 < C ? static_cast<int>(p.M - m0) : C;
+    if (p.bf16) {
+        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.y) + (m0 + K0) * p.N + n;
+#pragma unroll
+        for (int c = 0; c < C / 2; ++c, d += p.N)
+            if (K0 + c < live) *d = __float2bfloat16_rn(y[K0 + c] + part[(K0 + c) * 128] + bn);
+    } else {
+        float* d = static_cast<float*>(p.y) + (m0 + K0) * p.N + n;
+#pragma unroll
+        for (int c = 0; c < C / 2; ++c, d += p.N)
+            if (K0 + c < live) *d = y[K0 + c] + part[(K0 + c) * 128] + bn;
+    }
+}
+
+// Columns c0 .. c1 - 1 (tokens) of a split tile: the sums [column][weight row] of `split` CTAs added
+// in rank order; the draining warps' threads, G groups of 128.
+template <int TN, int G>
+__device__ __forceinline__ void store_share(const Fp8Params& p, const float* sums, uint32_t t, int c0, int c1,
+                                            uint32_t split) {
+    const int row = threadIdx.x & 127, g = (threadIdx.x - 128) >> 7;
+    const int64_t n = static_cast<int64_t>(t / p.tiles_m) * 128 + row, m0 = static_cast<int64_t>(t % p.tiles_m) * TN;
+    if (n >= p.N) return;
+    if (p.M - m0 < c1) c1 = static_cast<int>(p.M - m0);
+    const float bn = p.bias ? __ldcg(p.bias + n) : 0.0f;
+    // eight columns' remote reads in flight (one at a time, 128 columns of two CTAs took 5 us)
+    for (int c = c0 + g; c < c1; c += 8 * G) {
+        float v[8] = {};
+        for (uint32_t k = 0; k < split; ++k) {
+            float r[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[e] = c + e * G < c1 ? ld_shared_cluster_f32(sums + (c + e * G) * 128 + row, k) : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += r[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (c + e * G >= c1) break;
+            const int64_t at = (m0 + c + e * G) * p.N + n;
+            if (p.bf16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v[e] + bn);
+            else static_cast<float*>(p.y)[at] = v[e] + bn;
+        }
+    }
+}
+
+template <int TN>
+__global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __grid_constant__ Fp8Params p) {
+    using T = Tok<TN>;
+    constexpr int kStages = T::kStages, kStageBytes = T::kStageBytes, kNBuf = T::kNBuf, kCols = T::kCols,
+                  kChunk = T::kChunk, kSetWarps = T::kSetWarps;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+    // by an offset, not by a cast of the address: the compiler then knows it for shared memory (through
+    // generic loads the factors cost 512 x 8192 -> 2048 35 us for 31)
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::kOffBar);
     uint64_t* empty = full + kStages;
     uint64_t* tfull = empty + kStages;
-    uint64_t* tempty = tfull + 2;
-    uint64_t* drain = tempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* sfull = tfull + kNBuf;
+    uint64_t* sempty = sfull + 2;
+    uint64_t* drain = sempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    float* factors = reinterpret_cast<float*>(smem + T::kOffScale);
+    float* raw = reinterpret_cast<float*>(smem + T::kOffRaw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns};
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 1 + kSetWarps);  // the copies, and a set's release of the accumulator
             mbar_init(&empty[s], 1);
         }
+        for (int i = 0; i < kNBuf; ++i) mbar_init(&tfull[i], 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 4);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&sempty[i], 2 * kSetWarps);
+            mbar_init(&drain[i], 1);
         }
-        mbar_init(drain, 1);
         *abort_flag = 0u;
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, 2 * kBN);
+        tmem_alloc(tmem_slot, T::kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -135,102 +219,185 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     const uint32_t tmem = *tmem_slot;
     griddep_launch_dependents();
     griddep_wait();
-    const int tiles = p.tiles_m * p.tiles_n;
+    // this CTA's share of K, and its tiles (one for a cluster that splits K)
+    const uint32_t split = static_cast<uint32_t>(p.split), rank = blockIdx.x % split;
+    const int per = (p.nb + p.split - 1) / p.split, kb0 = static_cast<int>(rank) * per;
+    const int nb = p.nb - kb0 < per ? (p.nb - kb0 > 0 ? p.nb - kb0 : 0) : per;
+    const uint32_t tiles = static_cast<uint32_t>(p.tiles_m) * static_cast<uint32_t>(p.tiles_n);
+    const uint32_t first = blockIdx.x / split, step = gridDim.x / split;
+    const uint32_t total = tiles > first ? ((tiles - 1 - first) / step + 1) * static_cast<uint32_t>(nb) : 0u;
 
+    if (warp < 4) {
+    if constexpr (T::kResplit) regs_dec<kRegsLow>();
     if (warp == 0) {
         if (lane == 0) {
             uint32_t j = 0, issued = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                const int m0 = (t % p.tiles_m) * kBM, n0 = (t / p.tiles_m) * kBN;
-                for (int b = 0; b < p.nb; ++b, ++j) {
+            for (uint32_t t = first; ok && t < tiles; t += step) {
+                const int m0 = static_cast<int>(t % p.tiles_m) * TN, n0 = static_cast<int>(t / p.tiles_m) * 128;
+#pragma unroll 1
+                for (int b = 0; b < nb; ++b, ++j) {
                     const uint32_t s = j % kStages, k = j / kStages;
                     if (k > 0 && !mbar_poll(&empty[s], (k - 1) & 1, ctl)) {
                         ok = false;
                         break;
                     }
                     mbar_arrive_expect_tx(&full[s], kStageBytes);
-                    tma_load_2d(smem + s * kStageBytes, &p.amap, b * 128, m0, &full[s]);
-                    tma_load_2d(smem + s * kStageBytes + kATile, &p.wmap, b * 128, n0, &full[s]);
+                    tma_load_2d(smem + s * kStageBytes, &p.wmap, (kb0 + b) * 128, n0, &full[s]);
+                    tma_load_2d(smem + s * kStageBytes + T::kWBytes, &p.amap, (kb0 + b) * 128, m0, &full[s]);
                     issued = j + 1;
                 }
             }
-            if (*abort_flag)
+            if (*abort_flag)  // let every copy already issued land before the CTA exits
                 for (uint32_t q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
-                    drain_wait(&full[q % kStages], (q / kStages) & 1, 100000000ull);
+                    drain_wait(&full[q % kStages], (q / kStages) & 1, 10000000ull);
         }
         __syncwarp();
-    } else if (warp == 1) {
-        constexpr uint32_t idesc = idesc_e4m3_f32(kBM, kBN);
-        uint32_t j = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            for (int b = 0; b < p.nb; ++b, ++j) {
-                const uint32_t s = j % kStages, buf = j & 1u, u = j >> 1;
-                ok = __all_sync(0xffffffffu, (u == 0 || mbar_poll(&tempty[buf], (u - 1) & 1, ctl)) &&
-                                                 mbar_poll(&full[s], (j / kStages) & 1, ctl));
-                if (!ok) break;
+    } else if (warp <= 2) {
+        constexpr uint32_t idesc = idesc_e4m3_f32(128, TN);
+        const uint32_t par = warp - 1;
+        const uint64_t dw0 = smem_desc(smem_u32(smem), 1024, kLayoutSw128);
+        const uint64_t dt0 = smem_desc(smem_u32(smem + T::kWBytes), 1024, kLayoutSw128);
+        // one thread runs the whole loop: elected anew for every block, a warp lost 100 cycles a block
+        if (elect_one()) {
+            uint32_t s = par, phase = 0, buf = par;
+#pragma unroll 1
+            for (uint32_t j = par; j < total; j += 2) {
+                if (!mbar_poll(&full[s], phase, ctl)) break;
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t sa = smem_u32(smem + s * kStageBytes);
-                    const uint64_t da = smem_desc(sa, 1024, kLayoutSw128);
-                    const uint64_t dw = smem_desc(sa + kATile, 1024, kLayoutSw128);
+                const uint64_t o = static_cast<uint64_t>((s * kStageBytes) >> 4);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_f8f6f4(tmem + buf * kBN, da + 2 * k, dw + 2 * k, idesc, k > 0);
-                    mma_commit(&empty[s]);
-                    mma_commit(&tfull[buf]);
+                for (int k = 0; k < 4; ++k) mma_f8f6f4(tmem + buf * TN, dw0 + o + 2 * k, dt0 + o + 2 * k, idesc, k > 0);
+                mma_commit(&tfull[buf]);
+                mma_commit(&empty[s]);
+                buf ^= 2u;
+                if ((s += 2) >= kStages) s -= kStages, phase ^= 1u;
+            }
+            mma_commit(&drain[par]);
+        }
+        __syncwarp();
+        drain_wait(&drain[par], 0, 100000000ull);
+    } else {
+        // the scales of a batch are copied while the factors of the one before are formed (a loader
+        // that waited for its loads held the drain up: 512 x 2048 -> 6144 took 30 us with one)
+        uint32_t j = 0;  // batches
+        uint32_t tn = first, bn = 0;  // the next batch to copy: tile, block
+        auto copy = [&](uint32_t buf) {
+            if (tn < tiles && nb > 0) {
+                const int64_t m0 = static_cast<int64_t>(tn % p.tiles_m) * TN;
+                const float* sw = p.sw + static_cast<int64_t>(tn / p.tiles_m) * p.nb + kb0 + bn;
+                const float* sa = p.sa + (kb0 + bn) * p.M + m0;
+                const int last = p.M - m0 < TN ? static_cast<int>(p.M - m0) - 1 : TN - 1;  // columns past M: unused
+                const int cnt = nb - static_cast<int>(bn) < kChunk ? nb - static_cast<int>(bn) : kChunk;
+                float* d = raw + buf * T::kRawFloats;
+#pragma unroll 1
+                for (int c = lane; c < TN; c += 32) {
+                    const float* src = sa + (c < last ? c : last);
+#pragma unroll 1
+                    for (int k = 0; k < cnt; ++k, src += p.M) cp_async4(d + k * TN + c, src);
+                }
+                if (lane < cnt) cp_async4(d + kChunk * TN + lane, sw + lane);
+                bn += kChunk;
+                if (static_cast<int>(bn) >= nb) bn = 0, tn += step;
+            }
+            cp_async_commit();
+        };
+        copy(0);
+        for (uint32_t t = first; t < tiles && !*abort_flag; t += step) {
+            for (int b0 = 0; b0 < nb; b0 += kChunk, ++j) {
+                const uint32_t buf = j & 1u, u = j >> 1;
+                const int cnt = nb - b0 < kChunk ? nb - b0 : kChunk;
+                copy(buf ^ 1u);
+                cp_async_wait<1>();
+                __syncwarp();
+                if (u > 0) (void)mbar_poll(&sempty[buf], (u - 1) & 1, ctl);
+                float* d = factors + buf * (kChunk * TN);
+                const float* r = raw + buf * T::kRawFloats;
+#pragma unroll 1
+                for (int k = 0; k < cnt; ++k) {
+                    const float w = r[kChunk * TN + k];
+#pragma unroll
+                    for (int c = 0; c < TN; c += 32)
+                        if (TN >= 32 || lane < TN) d[k * TN + c + lane] = r[k * TN + c + lane] * w;
                 }
                 __syncwarp();
+                if (lane == 0) mbar_arrive(&sfull[buf]);
             }
         }
-        if (elect_one()) mma_commit(drain);
+        cp_async_wait<0>();
         __syncwarp();
-        drain_wait(drain, 0, 100000000ull);
-    } else if (warp >= 4) {
-        const int q = warp & 3;
-        const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        uint32_t j = 0;
+    }
+    } else {
+        if constexpr (T::kResplit) regs_inc<kRegsHigh>();
+        // set, lane quarter, column group
+        const uint32_t set = (warp - 4) / kSetWarps;
+        const int q = warp & 3, g = ((warp - 4) % kSetWarps) >> 2;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(g * kCols);
+        float* part = reinterpret_cast<float*>(smem + T::kOffPart) + g * kCols * 128 + q * 32 + lane;
+        // the accumulators start free
+        if (lane == 0)
+            for (uint32_t b = set; b < kNBuf && b < total; b += 2) mbar_arrive(&full[b]);
+        uint32_t j0 = 0, js = 0;  // blocks of the tiles done, batches of factors used
+        // after a wait gave up this warp waits no more: its sums are then undefined (the status word
+        // says so), but it still meets every barrier of the sets and of the cluster
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            const int tn = t / p.tiles_m;
-            const int64_t m = static_cast<int64_t>(t % p.tiles_m) * kBM + q * 32 + lane;
-            const float* sa = p.sa + m;
-            const float* sw = p.sw + static_cast<int64_t>(tn) * p.nb;
-            float y[kBN];
+        for (uint32_t t = first; t < tiles; t += step, j0 += nb) {
+            float y[kCols];
 #pragma unroll
-            for (int c = 0; c < kBN; ++c) y[c] = 0.0f;
-            for (int b = 0; b < p.nb; ++b, ++j) {
-                const uint32_t buf = j & 1u;
-                const float f = m < p.M ? __ldcg(sa + static_cast<int64_t>(b) * p.M) * __ldcg(sw + b) : 0.0f;
-                if (!__all_sync(0xffffffffu, mbar_poll(&tfull[buf], (j >> 1) & 1, ctl))) {
-                    ok = false;
-                    break;
+            for (int c = 0; c < kCols; ++c) y[c] = 0.0f;
+            for (int b0 = 0; b0 < nb; b0 += kChunk, ++js) {
+                if (ok) ok = mbar_poll(&sfull[js & 1u], (js >> 1) & 1, ctl);
+                const float* f = factors + (js & 1u) * (kChunk * TN) + g * kCols;
+                const int end = nb - b0 < kChunk ? nb - b0 : kChunk;
+#pragma unroll 1
+                for (int i = (set ^ (j0 + b0)) & 1u; i < end; i += 2) {
+                    const uint32_t j = j0 + b0 + i, buf = j % kNBuf;
+                    if (ok) ok = mbar_poll(&tfull[buf], (j / kNBuf) & 1, ctl);
+                    __syncwarp();
+                    tc_fence_after();
+                    const uint32_t ta = tl + buf * TN;
+                    constexpr int kAt = kCols == 32 ? 32 : 16;  // columns read at a time
+#pragma unroll
+                    for (int c0 = 0; c0 < kCols; c0 += kAt) {
+                        uint32_t v[kAt];
+#pragma unroll
+                        for (int c = 0; c < kAt; c += 16) tmem_ld_32x32b_x16(ta + c0 + c, v + c);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < kAt; ++c) asm volatile("" : "+r"(v[c]));  // uses stay behind the wait
+                        if (c0 + kAt == kCols) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0 && j + kNBuf < total) mbar_arrive(&full[(j + kNBuf) % kStages]);
+                        }
+#pragma unroll
+                        for (int c = 0; c < kAt; c += 16) fold16(y + c0 + c, f + i * TN + c0 + c, v + c);
+                    }
                 }
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < kBN; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x16(tl + buf * kBN + c, v);
-                    tmem_ld_32x32b_x16(tl + buf * kBN + c + 16, v + 16);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) y[c + e] = fmaf(f, __uint_as_float(v[e]), y[c + e]);
-                }
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty[buf]);
+                if (lane == 0) mbar_arrive(&sempty[js & 1u]);
             }
-            if (!ok) break;
-#pragma unroll
-            for (int c = 0; c < kBN; c += 32) store_cols<true>(p, m, static_cast<int64_t>(tn) * kBN + c, y + c);
+            // each set hands half of its columns to the other, adds the half it is handed and stores it
+            const int64_t m0 = static_cast<int64_t>(t % p.tiles_m) * TN + g * kCols;
+            const int64_t n = static_cast<int64_t>(t / p.tiles_m) * 128 + q * 32 + lane;
+            if (set == 0) finish_cols<kCols, 0, 64 * kSetWarps>(p, part, y, m0, n, split > 1, t == first);
+            else finish_cols<kCols, kCols / 2, 64 * kSetWarps>(p, part, y, m0, n, split > 1, t == first);
         }
     }
     __syncwarp();
+    if (split > 1) {
+        cluster_sync_all();
+        const int share = TN / static_cast<int>(split);
+        if (warp >= 4)
+            store_share<TN, 2 * kSetWarps / 4>(p, reinterpret_cast<const float*>(smem + T::kOffPart), first,
+                                               static_cast<int>(rank) * share, (static_cast<int>(rank) + 1) * share, split);
+        cluster_sync_all();  // no CTA leaves while another may still read its sums
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * kBN);
+        tmem_dealloc(tmem, T::kTmemCols);
     }
 }
 
@@ -276,10 +443,7 @@ constexpr int kOffBias = kOffScale + 2 * kScaleFloats * 4;  // the tile's bias, 
 constexpr int kOffBar = kOffBias + 2 * kBN * 4;
 constexpr int kSmemBytes = kOffBar + 256 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
-// Register split: launch = 640 x 96 (checked at build time); the first four warps drop to 32,
-// the sixteen epilogue warps rise to 112: 128 * 32 + 512 * 112 = 640 * 96.
-constexpr int kRegsLow = 32, kRegsHigh = 112;
-static_assert(128 * kRegsLow + 512 * kRegsHigh == kThreads * 96, "register split");
+static_assert(kThreads == kSplitThreads, "register split");
 // A wait on parity P returns at once while the phase before P is still open, so all phases of a
 // stage must be waited for by one warp: the two issuers take the even and the odd stages.  And a
 // stage's barrier may count a release only once its previous phase is over: a block's accumulators
@@ -339,11 +503,30 @@ __device__ __forceinline__ void stage_out(const Fp8Params& p, uint8_t* box, int 
     }
 }
 
+// The same 32 x 32 outputs for rows of y that no 16-byte store fits: turned in the staging box, so that a
+// warp's stores run along a row.
+__device__ __forceinline__ void store_rows(const Fp8Params& p, uint8_t* box, int64_t m0, int64_t n0, const float* y,
+                                           int lane) {
+    float* b = reinterpret_cast<float*>(box);
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 32; ++c) b[lane * 32 + (c ^ lane)] = y[c];  // the exclusive or keeps the banks apart
+    __syncwarp();
+    const int64_t n = n0 + lane;
+    const int rows = p.M - m0 < 32 ? static_cast<int>(p.M - m0) : 32;
+    if (n >= p.N) return;
+    for (int r = 0; r < rows; ++r) {
+        const float v = b[r * 32 + (lane ^ r)];
+        if (p.bf16) static_cast<__nv_bfloat16*>(p.y)[(m0 + r) * p.N + n] = __float2bfloat16_rn(v);
+        else static_cast<float*>(p.y)[(m0 + r) * p.N + n] = v;
+    }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ Fp8Params p) {
     using namespace pair;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
     uint64_t* empty = full + kStages;
     uint64_t* tfull = empty + kStages;  // [accumulator]: 2 (block parity) + half of the columns
@@ -418,13 +601,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             const uint64_t da0 = smem_desc(smem_u32(smem), 1024, kLayoutSw128);
             const uint64_t dw0 = smem_desc(smem_u32(smem + kABytes), 1024, kLayoutSw128);
             const uint32_t d = tmem + par * kBN;
+            if (elect_one()) {  // one thread runs the whole loop
+                uint32_t s = par, phase = 0;
 #pragma unroll 1
-            for (uint32_t j = par; j < total; j += 2) {
-                if (*abort_flag) break;
-                const uint32_t s = j % kStages;
-                (void)mbar_poll(&full[s], (j / kStages) & 1, ctl);
-                tc_fence_after();
-                if (elect_one()) {
+                for (uint32_t j = par; j < total; j += 2) {
+                    if (!mbar_poll(&full[s], phase, ctl)) break;
+                    tc_fence_after();
                     const uint64_t o = static_cast<uint64_t>((s * kStageBytes) >> 4);
                     constexpr uint64_t half = (kWRows / 2) * 128 >> 4;
 #pragma unroll
@@ -435,10 +617,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                         mma_f8f6f4_pair(d + kBN / 2, da0 + o + 2 * k, dw0 + o + half + 2 * k, idesc, k > 0);
                     mma_commit_pair(&tfull[2 * par + 1]);
                     mma_commit_pair(&empty[s]);
+                    if ((s += 2) >= kStages) s -= kStages, phase ^= 1u;
                 }
-                __syncwarp();
+                mma_commit_pair(&drain[par]);
             }
-            if (elect_one()) mma_commit_pair(&drain[par]);
             __syncwarp();
             drain_wait(&drain[par], 0, 100000000ull);
         } else if (warp == 3) {
@@ -538,8 +720,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             if (mw >= p.M || n0 >= p.N) continue;
             uint8_t* box = smem + kOffOut + (warp - 4) * kOutBox;
             if (!p.vec) {
-                store_cols<false>(p, mw + lane, n0, y);
-                store_cols<false>(p, mw + lane, n0 + 32, y + 32);
+                store_rows(p, box, mw, n0, y, lane);
+                store_rows(p, box, mw, n0 + 32, y + 32, lane);
             } else if (p.bf16) {
                 stage_out<true>(p, box, static_cast<int>(mw), static_cast<int>(n0), y, lane);
             } else {
@@ -631,10 +813,68 @@ cudaError_t launch(Kernel kernel, int smem_bytes, bool* attr_done, int64_t grid,
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <int TN>
+cudaError_t run_tok(Fp8Params& p, const Fp8Args& a, int num_sms, cudaStream_t s) {
+    using T = Tok<TN>;
+    static bool attr_done[64] = {};
+    p.tiles_m = static_cast<int>((a.M + TN - 1) / TN);
+    p.tiles_n = static_cast<int>((a.N + 127) / 128);
+    if (!make_map(&p.amap, a.a, a.M, a.K, TN) || !make_map(&p.wmap, a.w, a.N, a.K, 128)) return cudaErrorInvalidValue;
+    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+    const int64_t grid = p.split > 1 ? tiles * p.split : (tiles < num_sms ? tiles : num_sms);
+    return launch(fp8_tok_kernel<TN>, T::kSmemBytes, attr_done, grid, T::kThreads, p.split, p, s);
+}
+
+cudaError_t run_pair(Fp8Params& p, const Fp8Args& a, int num_sms, cudaStream_t s) {
+    static bool attr_done[64] = {};
+    p.tiles_m = static_cast<int>((a.M + pair::kBM - 1) / pair::kBM);
+    p.tiles_n = static_cast<int>((a.N + pair::kBN - 1) / pair::kBN);
+    if (!make_map(&p.amap, a.a, a.M, a.K, 128) || !make_map(&p.wmap, a.w, a.N, a.K, pair::kWRows) ||
+        (p.vec && !make_out_map(&p.ymap, a.y, a.M, a.N, a.bf16)))
+        return cudaErrorInvalidValue;
+    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n, most = num_sms / 2;
+    return launch(fp8_pair_kernel, pair::kSmemBytes, attr_done, 2 * (tiles < most ? tiles : most), pair::kThreads, 1, p, s);
+}
+
+// Estimated time in us of a form: start, then waves of tiles, each of `blocks` K-blocks and an end.
+// Fitted to measurements (bf16 out, back-to-back launches): 256 x 256 pairs 13.4 us at 512 x 2048 ->
+// 6144 (one wave of 16 blocks), 14.7 at 4096 x 1024 -> 2048 (two of 8), 378 at 8192 x 4096 -> 14336
+// (24 of 32); 128-token tiles 18.1, 21.2; 64-token tiles 16.4, 22.2; and at 256 x 2048 -> 2048 12.3,
+// 10.4 and 7.0.
+double form_us(double start, double block, double end, int64_t tiles, int64_t slots, int64_t blocks) {
+    const int64_t waves = (tiles + slots - 1) / slots;
+    return start + static_cast<double>(waves) * (block * static_cast<double>(blocks) + end);
+}
+
+// The form a problem takes: 0 (pairs) or the token tile, and the CTAs that share a tile's K.
+struct Form {
+    int tn, split;
+};
+Form pick_form(int64_t M, int64_t N, int64_t nb, int num_sms) {
+    const int64_t n128 = (N + 127) / 128;
+    Form best{0, 1};
+    double us = form_us(5.0, 0.43, 1.4, ((M + 255) / 256) * ((N + 255) / 256), num_sms / 2, nb);
+    const int tns[4] = {16, 32, 64, 128};
+    const double block[4] = {0.17, 0.19, 0.23, 0.36}, end[4] = {0.2, 0.3, 0.75, 1.4};
+    for (int i = 0; i < 4; ++i) {
+        const int tn = tns[i];
+        const int64_t tiles = ((M + tn - 1) / tn) * n128;
+        for (int split = 1; split <= 8 && split <= nb; split *= 2) {
+            // a split has one tile to a cluster, all of them running at once
+            if (split > 1 && tiles * split > num_sms) break;
+            // handing the parts over: 32 x 2048 -> 2048 with 16-token tiles took 5.1, 4.8 and 4.6 us on one,
+            // two and four CTAs a tile, 512 x 6144 -> 1024 with 64-token tiles 13.6 and 10.7 on one and two
+            const double t = form_us(2.4 + (split > 1 ? 0.8 + 0.015 * tn : 0.0), block[i], end[i], tiles, num_sms,
+                                     (nb + split - 1) / split);
+            if (t < us) us = t, best = Form{tn, split};
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_linear(const Fp8Args& a, int num_sms, cudaStream_t s) {
-    static bool attr_done[2][64] = {};
     if (num_sms < 1) return cudaErrorInvalidValue;
     Fp8Params p;
     p.sa = a.sa;
@@ -648,24 +888,15 @@ cudaError_t launch_fp8_linear(const Fp8Args& a, int num_sms, cudaStream_t s) {
     p.nb = static_cast<int>((a.K + kGroup8 - 1) / kGroup8);
     p.status = a.status;
     p.wait_limit_ns = a.wait_limit_ns;
-    // 256 x 256 tiles where they fill the GPU, else 128 x 128 tiles.
-    const int64_t pairs = ((a.M + pair::kBM - 1) / pair::kBM) * ((a.N + pair::kBN - 1) / pair::kBN);
-    if (2 * pairs >= num_sms) {
-        p.tiles_m = static_cast<int>((a.M + pair::kBM - 1) / pair::kBM);
-        p.tiles_n = static_cast<int>((a.N + pair::kBN - 1) / pair::kBN);
-        if (!make_map(&p.amap, a.a, a.M, a.K, 128) || !make_map(&p.wmap, a.w, a.N, a.K, pair::kWRows) ||
-            (p.vec && !make_out_map(&p.ymap, a.y, a.M, a.N, a.bf16)))
-            return cudaErrorInvalidValue;
-        const int64_t most = num_sms / 2;
-        return launch(fp8_pair_kernel, pair::kSmemBytes, attr_done[1], 2 * (pairs < most ? pairs : most), pair::kThreads, 1,
-                      p, s);
+    const Form f = pick_form(a.M, a.N, p.nb, num_sms);
+    p.split = f.split;
+    switch (f.tn) {
+        case 0: return run_pair(p, a, num_sms, s);
+        case 16: return run_tok<16>(p, a, num_sms, s);
+        case 32: return run_tok<32>(p, a, num_sms, s);
+        case 64: return run_tok<64>(p, a, num_sms, s);
+        default: return run_tok<128>(p, a, num_sms, s);
     }
-    p.tiles_m = static_cast<int>((a.M + base::kBM - 1) / base::kBM);
-    p.tiles_n = static_cast<int>((a.N + base::kBN - 1) / base::kBN);
-    if (!make_map(&p.amap, a.a, a.M, a.K, base::kBM) || !make_map(&p.wmap, a.w, a.N, a.K, base::kBN))
-        return cudaErrorInvalidValue;
-    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-    return launch(fp8_gemm_kernel, base::kSmemBytes, attr_done[0], tiles < num_sms ? tiles : num_sms, kThreads, 1, p, s);
 }
 
 }  // namespace w4a8
