@@ -56,7 +56,8 @@ def guarded(shape, dtype, fill=0x5A):
 
 
 ROWS = [(1, 64), (3, 128), (5, 192), (1, 4096), (7, 2048), (129, 1024), (300, 320), (33, 6144), (9, 14336),
-        (200, 8256), (3, 32768), (2, 33024), (153, 40960)]
+        (200, 8256), (3, 32768), (2, 33024), (153, 40960),
+        (7400, 2048), (3700, 2112), (1900, 14336)]
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
@@ -80,7 +81,7 @@ def test_norm_int8(M, K, with_res, dt):
 
 
 E_ROWS = [(1, 16), (3, 48), (2, 128), (1, 4096), (7, 2064), (129, 1024), (300, 336), (33, 6160), (9, 14336),
-          (3, 32768), (2, 33040), (153, 40960)]
+          (3, 32768), (2, 33040), (153, 40960), (3700, 2064), (1900, 14320)]
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
@@ -212,6 +213,32 @@ def test_prepared_operand_equals_codes(M):
                 mag = y0.abs().max()
                 assert (y0 - y1).abs().max() <= 1e-5 * mag
     assert torch.equal(out, (x.float() + res.float()).to(BF))
+
+
+@pytest.mark.parametrize("dt,with_res", [(BF, True), (BF, False), (F32, True)])
+def test_prepared_operand_of_many_rows(dt, with_res):
+    from w4a8_block_quantized_gb300 import synth
+    M, K, N = 7400, 2048, 128
+    d = synth.make_weights(synth.LinearSpec("w", M, K, N, True, 20.0, 6, 0))
+    wq, sw, zw, bias = (torch.from_numpy(np.ascontiguousarray(v)).cuda() for v in d[1:])
+    x, w = hidden(M, M, K, dt), 1 + 0.1 * normal(3, K)
+    res = normal(4, M, K).to(dt) if with_res else None
+    act, out = B().rmsnorm_prepare(x, w, EPS, residual=res)
+    codes = B().rmsnorm_quant(x, w, EPS, residual=res)
+    y = B().linear(*codes[:3], wq, sw, zw, bias)
+    assert torch.equal(y, B().linear_prepared(act, B().prepare_weights(wq, sw, zw), M, N, K, bias))
+    assert out is None if res is None else torch.equal(out, codes[3])
+
+
+def test_a_row_has_the_same_bits_in_any_batch():
+    """Scales too: the sum of squares is taken in an order that depends on the row's length alone."""
+    K = 4160
+    x, res, w = hidden(1, 4000, K, BF), normal(2, 4000, K).to(BF), 1 + 0.1 * normal(3, K)
+    big = B().rmsnorm_quant(x, w, EPS, residual=res)
+    for m0, m1 in ((0, 1), (7, 10), (100, 400), (0, 1500)):
+        part = B().rmsnorm_quant(x[m0:m1].contiguous(), w, EPS, residual=res[m0:m1].contiguous())
+        for a, b in zip(part, big):
+            assert torch.equal(a, b[m0:m1])
 
 
 def test_residual_in_place():

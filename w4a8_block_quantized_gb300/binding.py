@@ -29,6 +29,7 @@ OUT_F32 = 0
 OUT_BF16 = 1
 _OUT_DTYPES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
 _IN_DTYPES = {torch.float32: 0, torch.bfloat16: 1}   # W4A8_IN_F32, W4A8_IN_BF16
+_E8, _F32, _I8, _I32 = torch.float8_e4m3fn, torch.float32, torch.int8, torch.int32
 
 # name -> (restype, argtypes); every symbol include/w4a8.h declares
 _P = ctypes.c_void_p
@@ -507,25 +508,17 @@ def linear_act(act, wq, w_scale, w_zero, M: int, N: int, K: int, bias=None, y=No
 
 # ---------------------------------------------------------------- operators around the linears
 # These calls are short on the GPU (a few microseconds for a token), so what Python does around
-# the library call counts.  Each checks its tensors with `_fits`, a pass over cheap attributes
-# that allocates nothing, and goes through the checks that name the offending argument only where
-# that fails; addresses are passed as plain integers; and the current stream is taken as a raw
-# handle.  Measured on the GPU's host, one token through rmsnorm_quant: 13.7 -> 6.2 us a call (the
-# library call itself 2.6; a stream object alone costs 2.8, the raw handle 0.08).
+# the library call counts.  Where every output is given, a call checks its tensors in one
+# expression over cheap attributes; where that fails (or outputs are to be allocated) it goes
+# through the checks that name the offending argument.  Addresses are passed as plain integers,
+# and the current stream is taken as a raw handle.  Measured on the GPU's host, one token through
+# rmsnorm_quant: 13.7 -> 6.3 us a call (the library call itself 2.6; a stream object alone costs 2.8,
+# the raw handle 0.08).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _handle(index: int, stream) -> int:
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-
-
-def _fits(index: int, *args) -> bool:
-    """Whether every (tensor, dtype, shape) is a contiguous CUDA tensor of that dtype and shape on
-    device `index`, the current device."""
-    try:
-        for t, dtype, shape in args:
-            if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
-                return False
-    except AttributeError:
-        return False
-    return index == torch.cuda.current_device()
+    return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
 def _adr(t):
@@ -587,25 +580,50 @@ def _gate_up(gate, up):
 
 
 def _int8_out(M, K, dev, a_q, a_scale, rowsum):
-    a_q = torch.empty((M, K), dtype=torch.int8, device=dev) if a_q is None else a_q
-    a_scale = torch.empty((M,), dtype=torch.float32, device=dev) if a_scale is None else a_scale
-    rowsum = torch.empty((M, K // 64), dtype=torch.int32, device=dev) if rowsum is None else rowsum
-    if not _fits(dev.index, (a_q, torch.int8, (M, K)), (a_scale, torch.float32, (M,)),
-                 (rowsum, torch.int32, (M, K // 64))):
-        _arg(a_q, torch.int8, (M, K), "a_q", dev)
-        _arg(a_scale, torch.float32, (M,), "a_scale", dev)
-        _arg(rowsum, torch.int32, (M, K // 64), "rowsum", dev)
+    a_q = torch.empty((M, K), dtype=_I8, device=dev) if a_q is None else a_q
+    a_scale = torch.empty((M,), dtype=_F32, device=dev) if a_scale is None else a_scale
+    rowsum = torch.empty((M, K // 64), dtype=_I32, device=dev) if rowsum is None else rowsum
+    _arg(a_q, _I8, (M, K), "a_q", dev)
+    _arg(a_scale, _F32, (M,), "a_scale", dev)
+    _arg(rowsum, _I32, (M, K // 64), "rowsum", dev)
     return a_q, a_scale, rowsum
 
 
 def _e4m3_out(M, K, dev, a_q, a_scale):
     nb = (K + 127) // 128
-    a_q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev) if a_q is None else a_q
-    a_scale = torch.empty((nb, M), dtype=torch.float32, device=dev) if a_scale is None else a_scale
-    if not _fits(dev.index, (a_q, torch.float8_e4m3fn, (M, K)), (a_scale, torch.float32, (nb, M))):
-        _arg(a_q, torch.float8_e4m3fn, (M, K), "a_q", dev)
-        _arg(a_scale, torch.float32, (nb, M), "a_scale", dev)
+    a_q = torch.empty((M, K), dtype=_E8, device=dev) if a_q is None else a_q
+    a_scale = torch.empty((nb, M), dtype=_F32, device=dev) if a_scale is None else a_scale
+    _arg(a_q, _E8, (M, K), "a_q", dev)
+    _arg(a_scale, _F32, (nb, M), "a_scale", dev)
     return a_q, a_scale
+
+
+def _fits_int8(index, M, K, a_q, a_scale, rowsum) -> bool:
+    """Whether the three outputs of the INT8 form are given and fit, on the current device `index`."""
+    return a_q.dtype is _I8 and a_scale.dtype is _F32 and rowsum.dtype is _I32 and \
+        a_q.shape == (M, K) and a_scale.shape == (M,) and rowsum.shape == (M, K // 64) and \
+        a_q.get_device() == index and a_scale.get_device() == index and rowsum.get_device() == index and \
+        a_q.is_contiguous() and a_scale.is_contiguous() and rowsum.is_contiguous() and \
+        index == torch.cuda.current_device()
+
+
+def _fits_e4m3(index, M, K, a_q, a_scale) -> bool:
+    """The same for the two outputs of the e4m3 form."""
+    return a_q.dtype is _E8 and a_scale.dtype is _F32 and a_q.shape == (M, K) and \
+        a_scale.shape == ((K + 127) // 128, M) and a_q.get_device() == index and a_scale.get_device() == index and \
+        a_q.is_contiguous() and a_scale.is_contiguous() and index == torch.cuda.current_device()
+
+
+def _fits_norm(index, x, shape, dt, weight, residual, residual_out) -> bool:
+    """Whether all four tensors of a norm with a residual are given and fit."""
+    return weight.dtype is _F32 and residual.dtype is dt and residual_out.dtype is dt and \
+        weight.shape == shape[1:] and residual.shape == shape and residual_out.shape == shape and \
+        weight.get_device() == index and residual.get_device() == index and residual_out.get_device() == index and \
+        x.is_contiguous() and weight.is_contiguous() and residual.is_contiguous() and residual_out.is_contiguous()
+
+
+# what a missing or foreign argument raises in those expressions: the naming checks follow
+_NOT_FITTING = (AttributeError, KeyError, TypeError, ValueError)
 
 
 def _act_out(M, K, dev, act):
@@ -614,37 +632,33 @@ def _act_out(M, K, dev, act):
     return act
 
 
-def _norm(x, weight, residual, residual_out):
-    """_norm_in with the common case (every tensor given and fitting) checked in one pass."""
-    if residual is not None and residual_out is not None:
-        try:
-            dt, shape = x.dtype, x.shape
-            M, K = shape
-            code = _IN_DTYPES[dt]
-            if _fits(x.get_device(), (x, dt, shape), (weight, torch.float32, (K,)), (residual, dt, shape),
-                     (residual_out, dt, shape)):
-                return M, K, code, x.device, residual_out
-        except (AttributeError, KeyError, ValueError):
-            pass
-    return _norm_in(x, weight, residual, residual_out)
-
-
 def rmsnorm_quant(x, weight, eps, residual=None, residual_out=None, a_q=None, a_scale=None, rowsum=None, stream=None):
     """w4a8_rmsnorm_quant: rms_norm(x + residual) * weight as INT8 codes for `linear`.  Returns
     (a_q int8 [M,K], a_scale fp32 [M], rowsum int32 [M,K/64], x + residual or None)."""
-    M, K, code, dev, residual_out = _norm(x, weight, residual, residual_out)
-    a_q, a_scale, rowsum = _int8_out(M, K, dev, a_q, a_scale, rowsum)
-    rc = load().w4a8_rmsnorm_quant(x.data_ptr(), _adr(residual), weight.data_ptr(), eps, code, _adr(residual_out),
-                                   a_q.data_ptr(), a_scale.data_ptr(), rowsum.data_ptr(), M, K,
-                                   _handle(dev.index, stream))
-    _check(rc, "w4a8_rmsnorm_quant")
+    try:
+        M, K = shape = x.shape
+        index, dt = x.get_device(), x.dtype
+        code = _IN_DTYPES[dt]
+        fits = _fits_norm(index, x, shape, dt, weight, residual, residual_out) and \
+            _fits_int8(index, M, K, a_q, a_scale, rowsum)
+    except _NOT_FITTING:
+        fits = False
+    if not fits:
+        M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out)
+        a_q, a_scale, rowsum = _int8_out(M, K, dev, a_q, a_scale, rowsum)
+        index = dev.index
+    rc = (_lib or load()).w4a8_rmsnorm_quant(
+        x.data_ptr(), _adr(residual), weight.data_ptr(), eps, code, _adr(residual_out), a_q.data_ptr(),
+        a_scale.data_ptr(), rowsum.data_ptr(), M, K, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "w4a8_rmsnorm_quant")
     return a_q, a_scale, rowsum, residual_out
 
 
 def rmsnorm_prepare(x, weight, eps, residual=None, residual_out=None, act=None, stream=None):
     """w4a8_rmsnorm_prepare: rms_norm(x + residual) * weight as the opaque operand of
     `linear_prepared` and `linear_act`.  Returns (act, x + residual or None)."""
-    M, K, code, dev, residual_out = _norm(x, weight, residual, residual_out)
+    M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out)
     act = _act_out(M, K, dev, act)
     rc = load().w4a8_rmsnorm_prepare(x.data_ptr(), _adr(residual), weight.data_ptr(), eps, code, _adr(residual_out),
                                      act.data_ptr(), _nbytes(act), M, K, _handle(dev.index, stream))
@@ -655,11 +669,23 @@ def rmsnorm_prepare(x, weight, eps, residual=None, residual_out=None, act=None, 
 def rmsnorm_quant_fp8(x, weight, eps, residual=None, residual_out=None, a_q=None, a_scale=None, stream=None):
     """w4a8_rmsnorm_quant_fp8: rms_norm(x + residual) * weight as e4m3 codes for `fp8_linear`.
     Returns (a_q e4m3 [M,K], a_scale fp32 [ceil(K/128),M], x + residual or None)."""
-    M, K, code, dev, residual_out = _norm(x, weight, residual, residual_out)
-    a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
-    rc = load().w4a8_rmsnorm_quant_fp8(x.data_ptr(), _adr(residual), weight.data_ptr(), eps, code, _adr(residual_out),
-                                       a_q.data_ptr(), a_scale.data_ptr(), M, K, _handle(dev.index, stream))
-    _check(rc, "w4a8_rmsnorm_quant_fp8")
+    try:
+        M, K = shape = x.shape
+        index, dt = x.get_device(), x.dtype
+        code = _IN_DTYPES[dt]
+        fits = _fits_norm(index, x, shape, dt, weight, residual, residual_out) and \
+            _fits_e4m3(index, M, K, a_q, a_scale)
+    except _NOT_FITTING:
+        fits = False
+    if not fits:
+        M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out)
+        a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
+        index = dev.index
+    rc = (_lib or load()).w4a8_rmsnorm_quant_fp8(
+        x.data_ptr(), _adr(residual), weight.data_ptr(), eps, code, _adr(residual_out), a_q.data_ptr(),
+        a_scale.data_ptr(), M, K, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "w4a8_rmsnorm_quant_fp8")
     return a_q, a_scale, residual_out
 
 
@@ -687,11 +713,23 @@ def swiglu_prepare(gate, up, act=None, stream=None):
 def swiglu_quant_fp8(gate, up, a_q=None, a_scale=None, stream=None):
     """w4a8_swiglu_quant_fp8: silu(gate) * up as e4m3 codes for `fp8_linear`.  Returns
     (a_q e4m3 [M,K], a_scale fp32 [ceil(K/128),M])."""
-    M, K, ld, code, dev = _gate_up(gate, up)
-    a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
-    rc = load().w4a8_swiglu_quant_fp8(gate.data_ptr(), up.data_ptr(), ld, code, a_q.data_ptr(), a_scale.data_ptr(),
-                                      M, K, _handle(dev.index, stream))
-    _check(rc, "w4a8_swiglu_quant_fp8")
+    try:
+        M, K = shape = gate.shape
+        index, dt, strides = gate.get_device(), gate.dtype, gate.stride()
+        code, ld = _IN_DTYPES[dt], strides[0]
+        fits = up.shape == shape and up.dtype is dt and up.get_device() == index and up.stride() == strides and \
+            strides[1] == 1 and ld >= K and _fits_e4m3(index, M, K, a_q, a_scale)
+    except _NOT_FITTING:
+        fits = False
+    if not fits:
+        M, K, ld, code, dev = _gate_up(gate, up)
+        a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
+        index = dev.index
+    rc = (_lib or load()).w4a8_swiglu_quant_fp8(
+        gate.data_ptr(), up.data_ptr(), ld, code, a_q.data_ptr(), a_scale.data_ptr(), M, K,
+        _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "w4a8_swiglu_quant_fp8")
     return a_q, a_scale
 
 
@@ -727,23 +765,27 @@ def _fp8_in(a_q, a_scale, w_q, w_scale, bias, y, out_dtype):
 def fp8_linear(a_q, a_scale, w_q, w_scale, bias=None, y=None, out_dtype=None, stream=None):
     """w4a8_fp8_linear: e4m3 activations [M,K] with a_scale fp32 [ceil(K/128),M], e4m3 weights
     [N,K] with w_scale fp32 [ceil(N/128),ceil(K/128)] -> y fp32 or bf16 [M,N]."""
-    fits = False
-    if y is not None:
-        try:
-            e8, f32 = torch.float8_e4m3fn, torch.float32
-            (M, K), (N, _) = a_q.shape, w_q.shape
-            nb, dev = (K + 127) // 128, a_q.get_device()
-            args = (a_q, e8, (M, K)), (a_scale, f32, (nb, M)), (w_q, e8, (N, K)), (w_scale, f32, ((N + 127) // 128, nb))
-            fits = y.dtype in _OUT_DTYPES and _fits(dev, *args, (y, y.dtype, (M, N))) and \
-                (bias is None or _fits(dev, (bias, f32, (N,))))
-        except (AttributeError, ValueError):
-            fits = False
+    try:
+        (M, K), (N, _) = a_q.shape, w_q.shape
+        nb, index = (K + 127) // 128, a_q.get_device()
+        code = _OUT_DTYPES[y.dtype]
+        fits = a_q.dtype is _E8 and w_q.dtype is _E8 and a_scale.dtype is _F32 and w_scale.dtype is _F32 and \
+            a_scale.shape == (nb, M) and w_scale.shape == ((N + 127) // 128, nb) and w_q.shape == (N, K) and \
+            y.shape == (M, N) and w_q.get_device() == index and a_scale.get_device() == index and \
+            w_scale.get_device() == index and y.get_device() == index and a_q.is_contiguous() and \
+            w_q.is_contiguous() and a_scale.is_contiguous() and w_scale.is_contiguous() and y.is_contiguous() and \
+            (bias is None or (bias.dtype is _F32 and bias.shape == (N,) and bias.get_device() == index and
+                              bias.is_contiguous())) and index == torch.cuda.current_device()
+    except _NOT_FITTING:
+        fits = False
     if not fits:
         M, N, K, y = _fp8_in(a_q, a_scale, w_q, w_scale, bias, y, out_dtype)
-        dev = y.get_device()
-    rc = load().w4a8_fp8_linear(a_q.data_ptr(), a_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), _adr(bias),
-                                y.data_ptr(), _OUT_DTYPES[y.dtype], M, N, K, _handle(dev, stream))
-    _check(rc, "w4a8_fp8_linear")
+        index, code = y.get_device(), _OUT_DTYPES[y.dtype]
+    rc = (_lib or load()).w4a8_fp8_linear(
+        a_q.data_ptr(), a_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), _adr(bias), y.data_ptr(), code,
+        M, N, K, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "w4a8_fp8_linear")
     return y
 
 

@@ -52,10 +52,9 @@ int set_act(RowArgs* a, void* act, size_t act_bytes) {
     return W4A8_OK;
 }
 
-int run_rows(RowSource src, RowForm form, int in_dtype, const RowArgs& a, void* stream) {
+int run_rows(RowSource src, RowForm form, int in_dtype, RowArgs a, void* stream) {
     int num_sms = 0;
-    uint32_t* status = nullptr;
-    const int rc = device_info(&num_sms, &status);
+    const int rc = device_info(&num_sms, &a.status);
     if (rc != W4A8_OK) return rc;
     return launch_row_quant(src, form, in_dtype == W4A8_IN_BF16, a, num_sms, static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess

@@ -40,6 +40,7 @@ struct RowArgs {
     int32_t* rowsum = nullptr;
     uint8_t* trec = nullptr;
     int tw = 128;
+    uint32_t* status = nullptr;
 };
 
 // bf16: the type of x, up, residual and residual_out (fp32 otherwise).

@@ -14,10 +14,13 @@
 // scales: the codes are formed and stored without waiting for it.  The sum is taken in fp32 in an
 // order that depends on K alone.
 //
-// A row is read once.  `W` warps hold it in registers, C chunks of 8 values a lane: 16-byte
-// loads, 8-byte stores of codes.  Rows past 32 warps x 4 chunks take the looping kernel, which
-// reads twice (the second time from L2).  What bounds it: HBM bytes for many rows, the latency
-// of one load -> reduce -> store chain for few.
+// A row is read once: `W` warps hold it in registers, C chunks of 8 values a lane (16-byte loads,
+// 8-byte stores of codes), straight from memory or, for many rows, through a ring of rows in shared
+// memory.  Rows past 16 warps x 4 chunks take the looping kernel, which reads twice (the second time
+// from L2).  What bounds it: HBM bytes for many rows (16384 x 4096 bf16 norm to e4m3: 73 us, 6.4 TB/s,
+// 96% of the copy rate; 8192 x 14336 bf16 gated activation 101 us, 5.9 TB/s, where the exponential and
+// reciprocal units and the issue rate come into it), the latency of one load -> reduce -> store chain
+// for few (1 x 4096: 2.5 us).
 #include "ops_internal.h"
 #include "quant_math.cuh"
 #include "sm103_ptx.cuh"
@@ -28,27 +31,43 @@
 namespace w4a8 {
 namespace {
 
-// 8 consecutive values.
+// 8 consecutive values, as loaded and as fp32.
+template <bool BF16>
+struct Raw {
+    uint4 w[BF16 ? 1 : 2];
+};
 struct Chunk {
     float v[8];
 };
 
 template <bool BF16>
-__device__ __forceinline__ Chunk load_chunk(const void* p, int64_t idx) {
-    Chunk c;
+__device__ __forceinline__ Raw<BF16> load_raw(const void* p, int64_t idx) {
+    Raw<BF16> r;
     if constexpr (BF16) {
-        const uint4 w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + idx));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        r.w[0] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + idx));
+    } else {
+        const uint4* f = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + idx);
+        r.w[0] = __ldcs(f);
+        r.w[1] = __ldcs(f + 1);
+    }
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ Chunk values(const Raw<BF16>& r) {
+    Chunk c;
+#pragma unroll
+    for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
+        const uint32_t u[4] = {r.w[h].x, r.w[h].y, r.w[h].z, r.w[h].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            c.v[2 * i] = __uint_as_float(u[i] << 16);
-            c.v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            if constexpr (BF16) {
+                c.v[2 * i] = __uint_as_float(u[i] << 16);
+                c.v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            } else {
+                c.v[4 * h + i] = __uint_as_float(u[i]);
+            }
         }
-    } else {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + idx);
-        const float4 a = __ldcs(f), b = __ldcs(f + 1);
-        c.v[0] = a.x, c.v[1] = a.y, c.v[2] = a.z, c.v[3] = a.w;
-        c.v[4] = b.x, c.v[5] = b.y, c.v[6] = b.z, c.v[7] = b.w;
     }
     return c;
 }
@@ -71,28 +90,52 @@ __device__ __forceinline__ void store_chunk(void* p, int64_t idx, const Chunk& c
     }
 }
 
+// What a chunk is computed from, loaded for all of a lane's chunks before any is worked on: the
+// residual's stores would otherwise keep the next chunk's loads behind them (they may alias).
+template <int SRC, bool BF16>
+struct Inputs {
+    Raw<BF16> x, y;  // y: the residual, or up
+};
+
+template <int SRC, bool BF16>
+__device__ __forceinline__ void load_inputs(const RowArgs& a, int64_t m, int64_t k, Inputs<SRC, BF16>& in) {
+    in.x = load_raw<BF16>(a.x, m * a.ld + k);
+    if (SRC == kSrcNorm && a.residual) in.y = load_raw<BF16>(a.residual, m * a.K + k);
+    if (SRC == kSrcSwiglu) in.y = load_raw<BF16>(a.up, m * a.ld + k);
+}
+
+template <int SRC>
+__device__ __forceinline__ Chunk load_gamma(const RowArgs& a, int64_t k) {
+    Chunk c = {};
+    if constexpr (SRC == kSrcNorm) {
+        const float4* gp = reinterpret_cast<const float4*>(a.gamma + k);
+        const float4 g0 = gp[0], g1 = gp[1];
+        c.v[0] = g0.x, c.v[1] = g0.y, c.v[2] = g0.z, c.v[3] = g0.w;
+        c.v[4] = g1.x, c.v[5] = g1.y, c.v[6] = g1.z, c.v[7] = g1.w;
+    }
+    return c;
+}
+
 // The chunk at column k of row m: t in `t`, and its share of the sum of squares added to `sum`.
 // STORE: the residual sum is stored too.
 template <int SRC, bool BF16, bool STORE>
-__device__ __forceinline__ void source(const RowArgs& a, int64_t m, int64_t k, Chunk& t, float& sum) {
-    t = load_chunk<BF16>(a.x, m * a.ld + k);
+__device__ __forceinline__ void source(const RowArgs& a, int64_t m, int64_t k, const Inputs<SRC, BF16>& in,
+                                       const Chunk& gamma, Chunk& t, float& sum) {
+    t = values(in.x);
     if constexpr (SRC == kSrcNorm) {
         if (a.residual) {
-            const Chunk r = load_chunk<BF16>(a.residual, m * a.K + k);
+            const Chunk r = values(in.y);
 #pragma unroll
             for (int i = 0; i < 8; ++i) t.v[i] = __fadd_rn(t.v[i], r.v[i]);
             if (STORE && a.residual_out) store_chunk<BF16>(a.residual_out, m * a.K + k, t);
         }
-        const float4* gp = reinterpret_cast<const float4*>(a.gamma + k);
-        const float4 g0 = gp[0], g1 = gp[1];
-        const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             sum = fmaf(t.v[i], t.v[i], sum);
-            t.v[i] = __fmul_rn(t.v[i], g[i]);
+            t.v[i] = __fmul_rn(t.v[i], gamma.v[i]);
         }
     } else if constexpr (SRC == kSrcSwiglu) {
-        const Chunk u = load_chunk<BF16>(a.up, m * a.ld + k);
+        const Chunk u = values(in.y);
         // g / (1 + exp(-g)): for g below -88 exp(-g) is infinite and the quotient 0, its limit
 #pragma unroll
         for (int i = 0; i < 8; ++i) t.v[i] = __fdividef(t.v[i], 1.0f + __expf(-t.v[i])) * u.v[i];
@@ -111,47 +154,122 @@ __device__ __forceinline__ float row_factor(float sum, int64_t K, float eps) {
     return __frcp_rn(__fsqrt_rn(__fdiv_rn(sum, static_cast<float>(K)) + eps));
 }
 
-// Codes of one e4m3 group held by 16 lanes (lanes of the other half warp: another group), and
-// its scale before the factor r.  Chunks past the row hold zeros.
-__device__ __forceinline__ float e4m3_group(const Chunk& t, uint2& codes) {
-    float m = chunk_max(t);
+// C values reduced over the lanes that differ in the bits below TOP (a power of two; C <= TOP), all at
+// once: each of the first steps sends half of a lane's values to its partner and keeps the rest, so C
+// values cost C - 1 + log2(TOP / C) + 1 shuffles rather than C log2(2 TOP).  The lane is left with value
+// slot<C, TOP>(lane); lane lane_of<C, TOP>(i) (and others) with value i.  Each value's tree pairs lanes at
+// distance TOP, then TOP / 2, ..., 1, whatever C.
+template <int C, int TOP>
+__device__ __forceinline__ int slot(int lane) {
+    return C == 4 ? ((lane & TOP) ? 2 : 0) + ((lane & (TOP / 2)) ? 1 : 0) : C == 2 ? ((lane & TOP) ? 1 : 0) : 0;
+}
+template <int C, int TOP>
+__device__ __forceinline__ int lane_of(int i) {
+    return C == 4 ? (i >> 1) * TOP + (i & 1) * (TOP / 2) : C == 2 ? i * TOP : 0;
+}
+template <int C, int TOP, typename Op>
+__device__ __forceinline__ float reduce(const float (&v)[C], int lane, Op&& op) {
+    float r;
+    int o = TOP;
+    if constexpr (C == 4) {
+        const bool u = lane & TOP, w = lane & (TOP / 2);
+        const float a0 = op(u ? v[2] : v[0], __shfl_xor_sync(0xffffffffu, u ? v[0] : v[2], TOP));
+        const float a1 = op(u ? v[3] : v[1], __shfl_xor_sync(0xffffffffu, u ? v[1] : v[3], TOP));
+        r = op(w ? a1 : a0, __shfl_xor_sync(0xffffffffu, w ? a0 : a1, TOP / 2));
+        o = TOP / 4;
+    } else if constexpr (C == 2) {
+        const bool u = lane & TOP;
+        r = op(u ? v[1] : v[0], __shfl_xor_sync(0xffffffffu, u ? v[0] : v[1], TOP));
+        o = TOP / 2;
+    } else {
+        r = v[0];
+    }
 #pragma unroll
-    for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const bool live = m >= 0x1p-100f;
-    const float inv = live ? __fdiv_rn(448.0f, m) : 0.0f;
-    float q[8];
+    for (; o; o >>= 1) r = op(r, __shfl_xor_sync(0xffffffffu, r, o));
+    return r;
+}
+struct Max {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct Add {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+
+// e4m3 codes of the C groups that this half warp holds (16 lanes, 8 columns each; chunks past the row
+// hold zeros).  The groups' largest magnitudes are reduced together, which leaves group
+// slot<C, 8>(lane) with the lane: one pair of divisions for all C groups (a pair each, and C separate
+// reductions, made the divisions a third of the kernel's instructions).  Returns that group's scale
+// before the factor r.
+template <int C>
+__device__ __forceinline__ float e4m3_groups(const Chunk (&t)[C], uint2 (&codes)[C], int lane) {
+    float m[C];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(t.v[i], inv);
-    codes.x = e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
-    codes.y = e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16);
-    return live ? __fdiv_rn(m, 448.0f) : 0.0f;
+    for (int i = 0; i < C; ++i) m[i] = chunk_max(t[i]);
+    const float mine = reduce<C, 8>(m, lane, Max());
+    const bool live = mine >= 0x1p-100f;
+    const float inv = live ? __fdiv_rn(448.0f, mine) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const float f = __shfl_sync(0xffffffffu, inv, (lane & 16) | lane_of<C, 8>(i));
+        float q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = __fmul_rn(t[i].v[e], f);
+        codes[i].x = e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
+        codes[i].y = e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16);
+    }
+    return live ? __fdiv_rn(mine, 448.0f) : 0.0f;
 }
 
-// INT8 codes of one chunk (q, as floats) into the API layout or a token record, and the sum of
-// each 64-block's codes, taken over its 8 lanes (exact: small integers).  All lanes take part.
+// INT8 codes of one chunk (as floats) into the API layout or a token record.
 template <int FORM>
-__device__ __forceinline__ void store_int8(const RowArgs& a, int64_t m, int64_t chunk, bool in, const float4& q0,
-                                           const float4& q1, int lane) {
-    float rs = ((q0.x + q0.y) + (q0.z + q0.w)) + ((q1.x + q1.y) + (q1.z + q1.w));
-#pragma unroll
-    for (int o = 4; o; o >>= 1) rs += __shfl_xor_sync(0xffffffffu, rs, o);
-    if (!in) return;
-    const int64_t nb = a.K / kBlock, b = chunk >> 3;
+__device__ __forceinline__ void store_int8(const RowArgs& a, int64_t m, int64_t chunk, const float4& q0, const float4& q1) {
     if constexpr (FORM == kFormInt8) {
         *reinterpret_cast<uint2*>(a.a_q + m * a.K + 8 * chunk) = make_uint2(bytes4f(q0), bytes4f(q1));
-        if ((lane & 7) == 0) a.rowsum[m * nb + b] = static_cast<int>(rs);
     } else {
         const int ts = a.tw == 256 ? 8 : 7;
         const int r = static_cast<int>(m & ((1 << ts) - 1)), j = 2 * static_cast<int>(chunk & 7);
-        uint8_t* rec = token_rec(a.trec, m, b, nb, ts);
+        uint8_t* rec = token_rec(a.trec, m, chunk >> 3, a.K / kBlock, ts);
         uint2 hi, lo;
         planes4f(q0, hi.x, lo.x);
         planes4f(q1, hi.y, lo.y);
         // quads j and j + 1 share a 16-byte chunk of the record (j is even): 8-byte stores
         *reinterpret_cast<uint2*>(rec + plane_off(r, j, 0)) = hi;
         *reinterpret_cast<uint2*>(rec + plane_off(r, j, 1)) = lo;
-        if ((lane & 7) == 0) *reinterpret_cast<uint4*>(rec + (128 << ts) + r * 16) = rx_entry(static_cast<int>(rs));
     }
+}
+
+// The sum of the codes of 64-block b of row m.
+template <int FORM>
+__device__ __forceinline__ void store_sum(const RowArgs& a, int64_t m, int64_t b, int rs) {
+    const int64_t nb = a.K / kBlock;
+    if constexpr (FORM == kFormInt8) {
+        a.rowsum[m * nb + b] = rs;
+    } else {
+        const int ts = a.tw == 256 ? 8 : 7;
+        *reinterpret_cast<uint4*>(token_rec(a.trec, m, b, nb, ts) + (128 << ts) + (m & ((1 << ts) - 1)) * 16) = rx_entry(rs);
+    }
+}
+
+// The C chunks' INT8 codes and the sums of their 64-blocks (8 lanes each; exact: small integers).
+template <int FORM, int C>
+__device__ __forceinline__ void int8_codes(const RowArgs& a, int64_t m, bool row, int64_t c0, int64_t by, int lane,
+                                           const Chunk (&t)[C], float s) {
+    const float inv = __frcp_rn(s);
+    const int64_t n8 = a.K / 8;
+    float sums[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const float4 x[2] = {make_float4(t[i].v[0], t[i].v[1], t[i].v[2], t[i].v[3]),
+                             make_float4(t[i].v[4], t[i].v[5], t[i].v[6], t[i].v[7])};
+        float4 q[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (s > 0.0f) quant_lane<2>(x, q, s, inv);
+        const int64_t c = c0 + i * by;
+        if (row && c < n8) store_int8<FORM>(a, m, c, q[0], q[1]);
+        sums[i] = ((q[0].x + q[0].y) + (q[0].z + q[0].w)) + ((q[1].x + q[1].y) + (q[1].z + q[1].w));
+    }
+    const float rs = reduce<C, 4>(sums, lane, Add());
+    const int64_t c = c0 + slot<C, 4>(lane) * by;  // a chunk of this lane's block
+    if ((lane & (8 / C - 1)) == 0 && row && c < n8) store_sum<FORM>(a, m, c >> 3, static_cast<int>(rs));
 }
 
 // The maximum over the row's W warps.  Of the row's sum of squares, each warp holds C segment
@@ -160,63 +278,42 @@ __device__ __forceinline__ void store_int8(const RowArgs& a, int64_t m, int64_t 
 // on how its segments were dealt to warps: a row has the same bits in any batch.
 // `red`: W maxima, then W C segment sums; only the row's warps meet.
 template <int C, bool SUM, bool MAX>
-__device__ __forceinline__ void row_reduce(float& amax, float (&sum)[C], float& total, float* red, int wg, int W,
+__device__ __forceinline__ void row_reduce(float& amax, const float (&sum)[C], float& total, float* red, int wg, int W,
                                            int bar, int lane) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        if (MAX) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (SUM) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-    }
-    float v = 0.0f;
+    float seg = 0.0f, v = 0.0f;
+    if (MAX) amax = reduce<1, 16>({amax}, lane, Max());
+    if (SUM) seg = reduce<C, 16>(sum, lane, Add());  // of segment slot<C, 16>(lane)
     if (W == 1) {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (lane == i) v = sum[i];
+        if (SUM) {
+            v = __shfl_sync(0xffffffffu, seg, lane_of<C, 16>(lane & (C - 1)));
+            if (lane >= C) v = 0.0f;
+        }
     } else {
-        if (lane == 0) {
-            if (MAX) red[wg] = amax;
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-                if (SUM) red[W + i * W + wg] = sum[i];
-        }
+        if (MAX && lane == 0) red[wg] = amax;
+        if (SUM && (lane & (32 / C - 1)) == 0) red[W + slot<C, 16>(lane) * W + wg] = seg;
         named_bar_sync(bar, W * 32);
-        if (MAX) {
-            amax = lane < W ? red[lane] : 0.0f;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        }
+        if (MAX) amax = reduce<1, 16>({lane < W ? red[lane] : 0.0f}, lane, Max());
         if (SUM)
             for (int j = lane; j < W * C; j += 32) v += red[W + j];
     }
-    if (SUM) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    }
-    total = v;
+    if (SUM) total = reduce<1, 16>({v}, lane, Add());
 }
 
-// One row per W warps, blockDim / (32 W) rows a block; C chunks a lane (K <= 256 W C).
-template <int SRC, int FORM, bool BF16, int C>
-__global__ void __launch_bounds__(1024) row_quant_kernel(const RowArgs a, int W) {
-    griddep_launch_dependents();
-    __shared__ float slots[32 * (1 + C)];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rsub = warp / W, wg = warp - rsub * W;
-    float* red = slots + rsub * W * (1 + C);
-    const int64_t m = static_cast<int64_t>(blockIdx.x) * ((blockDim.x >> 5) / W) + rsub;
-    const int64_t n8 = a.K / 8;
-    const bool row = m < a.M;  // the same for every warp of a row
-    griddep_wait();
+// One row (`row`: it exists), or its part from chunk `base` on, held by W warps, this one the wg-th:
+// chunk base + (i W + wg) 32 + lane is input(i), its gamma gamma(i), i < C.  After `read()` the inputs are in registers (of every lane
+// of this warp; the row's other warps meet in the reduction).
+template <int SRC, int FORM, bool BF16, int C, typename Input, typename Gamma, typename Read>
+__device__ __forceinline__ void work_row(const RowArgs& a, int64_t m, bool row, int64_t base, int W, int wg, int lane,
+                                         float* red, int bar, Input&& input, Gamma&& gamma, Read&& read) {
+    const int64_t n8 = a.K / 8, c0 = base + static_cast<int64_t>(wg) * 32 + lane, by = static_cast<int64_t>(W) * 32;
     Chunk t[C];
     float sum[C], amax = 0.0f, total = 0.0f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int64_t c = static_cast<int64_t>(i * W + wg) * 32 + lane;
+        const int64_t c = c0 + i * by;
         sum[i] = 0.0f;
         if (row && c < n8) {
-            source<SRC, BF16, true>(a, m, 8 * c, t[i], sum[i]);
+            source<SRC, BF16, true>(a, m, 8 * c, input(i), gamma(i), t[i], sum[i]);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[i].v[e] = 0.0f;
@@ -224,39 +321,141 @@ __global__ void __launch_bounds__(1024) row_quant_kernel(const RowArgs a, int W)
         if (FORM != kFormE4m3) amax = fmaxf(amax, chunk_max(t[i]));
     }
     if constexpr (FORM == kFormE4m3) {
-        float s[C];
+        uint2 codes[C];
+        const float s = e4m3_groups(t, codes, lane);
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const int64_t c = static_cast<int64_t>(i * W + wg) * 32 + lane;
-            uint2 codes;
-            s[i] = e4m3_group(t[i], codes);
-            if (row && c < n8) *reinterpret_cast<uint2*>(a.a_q + m * a.K + 8 * c) = codes;
-        }
+        for (int i = 0; i < C; ++i)
+            if (row && c0 + i * by < n8) *reinterpret_cast<uint2*>(a.a_q + m * a.K + 8 * (c0 + i * by)) = codes[i];
         float r = 1.0f;
         if constexpr (SRC == kSrcNorm) {
-            row_reduce<C, true, false>(amax, sum, total, red, wg, W, 1 + rsub, lane);
+            row_reduce<C, true, false>(amax, sum, total, red, wg, W, bar, lane);
             r = row_factor(total, a.K, a.eps);
         }
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const int64_t c = static_cast<int64_t>(i * W + wg) * 32 + lane;
-            if (row && c < n8 && (lane & 15) == 0) a.a_scale[(c >> 4) * a.M + m] = s[i] * r;
-        }
+        read();
+        const int64_t c = c0 - (lane & 15) + slot<C, 8>(lane) * by;  // the first chunk of this lane's group
+        if ((lane & (16 / C - 1)) == 0 && row && c < n8) a.a_scale[(c >> 4) * a.M + m] = s * r;
     } else {
-        row_reduce<C, SRC == kSrcNorm, true>(amax, sum, total, red, wg, W, 1 + rsub, lane);
+        row_reduce<C, SRC == kSrcNorm, true>(amax, sum, total, red, wg, W, bar, lane);
+        read();
         const float s = __fdiv_rn(amax, 127.0f);
-        const float inv = __frcp_rn(s);
-        if (row && wg == 0 && lane == 0)
-            a.a_scale[m] = SRC == kSrcNorm ? s * row_factor(total, a.K, a.eps) : s;
+        if (row && wg == 0 && lane == 0) a.a_scale[m] = SRC == kSrcNorm ? s * row_factor(total, a.K, a.eps) : s;
+        int8_codes<FORM, C>(a, m, row, c0, by, lane, t, s);
+    }
+}
+
+// The forms whose scales do not span the row (e4m3 without a norm) are worked on in parts of 256 C
+// columns, a warp each: blocks of any size then fit any row.
+template <int SRC, int FORM>
+constexpr bool kParts = SRC != kSrcNorm && FORM == kFormE4m3;
+
+// Straight into registers: a row per W warps (or a part per warp, W = 1), blockDim / (32 W) of them a
+// block; C chunks a lane (K <= 256 W C parts), all loaded before the first is worked on.
+template <int SRC, int FORM, bool BF16, int C>
+__global__ void __launch_bounds__(512) row_quant_kernel(const RowArgs a, int W, int parts) {
+    griddep_launch_dependents();
+    __shared__ float slots[16 * (1 + C)];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rsub = warp / W, wg = warp - rsub * W;
+    int64_t m = static_cast<int64_t>(blockIdx.x) * ((blockDim.x >> 5) / W) + rsub, base = 0;
+    if constexpr (kParts<SRC, FORM>) {
+        const int64_t item = m;
+        m = item / parts;
+        base = (item - m * parts) * (32 * C);
+    }
+    const int64_t n8 = a.K / 8, c0 = base + static_cast<int64_t>(wg) * 32 + lane, by = static_cast<int64_t>(W) * 32;
+    const bool row = m < a.M;  // the same for every warp of a row
+    griddep_wait();
+    Inputs<SRC, BF16> in[C];
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const int64_t c = static_cast<int64_t>(i * W + wg) * 32 + lane;
-            const float4 x[2] = {make_float4(t[i].v[0], t[i].v[1], t[i].v[2], t[i].v[3]),
-                                 make_float4(t[i].v[4], t[i].v[5], t[i].v[6], t[i].v[7])};
-            float4 q[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-            if (s > 0.0f) quant_lane<2>(x, q, s, inv);
-            store_int8<FORM>(a, m, c, row && c < n8, q[0], q[1], lane);
-        }
+    for (int i = 0; i < C; ++i)
+        if (row && c0 + i * by < n8) load_inputs<SRC, BF16>(a, m, 8 * (c0 + i * by), in[i]);
+    work_row<SRC, FORM, BF16, C>(
+        a, m, row, base, W, wg, lane, slots + rsub * W * (1 + C), 1 + rsub, [&](int i) { return in[i]; },
+        [&](int i) { return load_gamma<SRC>(a, 8 * (c0 + i * by)); }, [] {});
+}
+
+// Many rows: the rows come through shared memory, copied by the async engine `stages` rows ahead of each
+// group of W warps, so that the bytes in flight neither cost registers nor stop while a row is worked
+// on.  A group walks rows m, m + groups, ...; its first thread refills a stage once the group has read
+// it.  gamma stays in registers.  Shared memory: [group][stage][x | y][K], then a barrier per stage.
+template <int SRC, int FORM, bool BF16, int C>
+__global__ void __launch_bounds__(512) row_stream_kernel(const RowArgs a, int W, int stages) {
+    griddep_launch_dependents();
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float slots[2][16 * (1 + C)];
+    __shared__ uint32_t abort_flag;
+    constexpr int kEl = BF16 ? 2 : 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rsub = warp / W, wg = warp - rsub * W, rpc = static_cast<int>(blockDim.x >> 5) / W;
+    const bool two = SRC == kSrcSwiglu || (SRC == kSrcNorm && a.residual);
+    const uint32_t bytes = static_cast<uint32_t>(a.K) * kEl, stage_bytes = bytes * (two ? 2 : 1);
+    uint8_t* ring = smem + static_cast<uint32_t>(rsub * stages) * stage_bytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<uint32_t>(rpc * stages) * stage_bytes) + rsub * stages;
+    const WaitCtl ctl{&abort_flag, a.status, 1000000000ull};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < rpc * stages; ++i) mbar_init(full + i, 1);
+        abort_flag = 0u;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * rpc + rsub, step = static_cast<int64_t>(gridDim.x) * rpc;
+    const int64_t n8 = a.K / 8;
+    const bool leader = wg == 0 && lane == 0;
+    auto fill = [&](int64_t m, int s) {
+        mbar_arrive_expect_tx(full + s, stage_bytes);
+        bulk_load(ring + s * stage_bytes, static_cast<const uint8_t*>(a.x) + m * a.ld * kEl, bytes, full + s);
+        if (two)
+            bulk_load(ring + s * stage_bytes + bytes,
+                      SRC == kSrcNorm ? static_cast<const uint8_t*>(a.residual) + m * a.K * kEl
+                                      : static_cast<const uint8_t*>(a.up) + m * a.ld * kEl,
+                      bytes, full + s);
+    };
+    if (leader)
+        for (int s = 0; s < stages && first + s * step < a.M; ++s) fill(first + s * step, s);
+    Chunk gamma[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int64_t c = static_cast<int64_t>(i * W + wg) * 32 + lane;
+        if (c < n8) gamma[i] = load_gamma<SRC>(a, 8 * c);
+    }
+    // after a wait gave up the rest of the rows is worked on as it is (the status word says so); the
+    // stages in flight are left to land below
+    bool ok = true;
+    int s = 0, par = 0;
+    uint32_t phase = 0;
+    for (int64_t m = first; m < a.M; m += step, par ^= 1) {
+        if (ok) ok = mbar_wait(full + s, phase, ctl);
+        __syncwarp();
+        const uint8_t* st = ring + s * stage_bytes;
+        work_row<SRC, FORM, BF16, C>(
+            a, m, true, 0, W, wg, lane, slots[par] + rsub * W * (1 + C), 1 + rsub,
+            [&](int i) {
+                const uint32_t at = static_cast<uint32_t>((i * W + wg) * 32 + lane) * 8 * kEl;
+                Inputs<SRC, BF16> in;
+#pragma unroll
+                for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
+                    in.x.w[h] = *reinterpret_cast<const uint4*>(st + at + 16 * h);
+                    if (two) in.y.w[h] = *reinterpret_cast<const uint4*>(st + bytes + at + 16 * h);
+                }
+                return in;
+            },
+            [&](int i) { return gamma[i]; },
+            [&] {
+                if (SRC != kSrcNorm && FORM == kFormE4m3) {  // the forms without a reduction
+                    if (W > 1) named_bar_sync(1 + rsub, W * 32);
+                    else __syncwarp();
+                } else if (W == 1) {
+                    __syncwarp();
+                }
+                // every warp of the row has read the stage: its next row may land
+                if (leader && ok && m + stages * step < a.M) fill(m + stages * step, s);
+            });
+        if (++s == stages) s = 0, phase ^= 1u;
+    }
+    if (leader && !ok) {  // let what is in flight land (for a bounded time) before the block leaves
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(1000);
     }
 }
 
@@ -272,71 +471,114 @@ __global__ void __launch_bounds__(1024) row_quant_long_kernel(const RowArgs a) {
     float sum[1] = {0.0f}, amax = 0.0f, total = 0.0f;
     for (int64_t c = threadIdx.x; c < n8; c += 1024) {
         Chunk t;
-        source<SRC, BF16, false>(a, m, 8 * c, t, sum[0]);
+        Inputs<SRC, BF16> in;
+        load_inputs<SRC, BF16>(a, m, 8 * c, in);
+        source<SRC, BF16, false>(a, m, 8 * c, in, load_gamma<SRC>(a, 8 * c), t, sum[0]);
         if (FORM != kFormE4m3) amax = fmaxf(amax, chunk_max(t));
     }
     row_reduce<1, true, true>(amax, sum, total, red, warp, 32, 1, lane);
     const float r = SRC == kSrcNorm ? row_factor(total, a.K, a.eps) : 1.0f;
-    const float s = __fdiv_rn(amax, 127.0f), inv = __frcp_rn(s);
+    const float s = __fdiv_rn(amax, 127.0f);
     if (FORM != kFormE4m3 && threadIdx.x == 0) a.a_scale[m] = s * r;
     for (int64_t c0 = warp * 32; c0 < n8; c0 += 1024) {
         const int64_t c = c0 + lane;
         Chunk t;
         float unused = 0.0f;
         if (c < n8) {
-            source<SRC, BF16, true>(a, m, 8 * c, t, unused);
+            Inputs<SRC, BF16> in;
+            load_inputs<SRC, BF16>(a, m, 8 * c, in);
+            source<SRC, BF16, true>(a, m, 8 * c, in, load_gamma<SRC>(a, 8 * c), t, unused);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) t.v[e] = 0.0f;
         }
+        const Chunk tt[1] = {t};
         if constexpr (FORM == kFormE4m3) {
-            uint2 codes;
-            const float sg = e4m3_group(t, codes);
+            uint2 codes[1];
+            const float sg = e4m3_groups(tt, codes, lane);
             if (c < n8) {
-                *reinterpret_cast<uint2*>(a.a_q + m * a.K + 8 * c) = codes;
+                *reinterpret_cast<uint2*>(a.a_q + m * a.K + 8 * c) = codes[0];
                 if ((lane & 15) == 0) a.a_scale[(c >> 4) * a.M + m] = sg * r;
             }
         } else {
-            const float4 x[2] = {make_float4(t.v[0], t.v[1], t.v[2], t.v[3]),
-                                 make_float4(t.v[4], t.v[5], t.v[6], t.v[7])};
-            float4 q[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-            if (s > 0.0f) quant_lane<2>(x, q, s, inv);
-            store_int8<FORM>(a, m, c, c < n8, q[0], q[1], lane);
+            int8_codes<FORM, 1>(a, m, true, c, 0, lane, tt, s);
         }
     }
 }
 
-cudaError_t launch_pdl(void (*kernel)(RowArgs, int), int64_t grid, int threads, const RowArgs& a, int W, cudaStream_t s) {
+template <typename... Args>
+cudaError_t launch_pdl(void (*kernel)(Args...), int64_t grid, int threads, size_t smem, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, W);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Blocks per SM of the streaming kernel and rows in flight a group.  Measured on 16384 x 4096 bf16 (us):
+// two stages and 4 / 6 / 8 blocks 73.3 / 74.3 / 72.9, three stages (smaller blocks) 78.3, one 87.1; on
+// 4096 x 14336 4 / 6 / 8 blocks 70.7 / 76.1 / 76.8.
+constexpr int kStreamBlocks = 4, kStreamStages = 2;
+
+template <int FORM>
+cudaError_t run_stream(const RowArgs& a, int W, int rpc, int num_sms, cudaStream_t s) {
+    static bool attr_done[64] = {};
+    constexpr int kMost = 2 * 2 * 16384 * kStreamStages;  // the deepest row: bf16, two inputs, one row a block
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && !attr_done[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(row_stream_kernel<kSrcNorm, FORM, true, 4>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMost + 256);
+        if (e != cudaSuccess) return e;
+        attr_done[dev] = true;
+    }
+    const size_t stage = static_cast<size_t>(a.K) * 2 * (a.residual ? 2 : 1);
+    const size_t smem = static_cast<size_t>(rpc * kStreamStages) * (stage + 8);
+    const int64_t need = (a.M + rpc - 1) / rpc, cap = static_cast<int64_t>(num_sms) * kStreamBlocks;
+    const int64_t rounds = (need + cap - 1) / cap;
+    return launch_pdl(row_stream_kernel<kSrcNorm, FORM, true, 4>, (need + rounds - 1) / rounds, rpc * W * 32, smem, s, a, W,
+                      kStreamStages);
 }
 
 template <int SRC, int FORM, bool BF16>
 cudaError_t run(const RowArgs& a, int num_sms, cudaStream_t s) {
     const int64_t n8 = a.K / 8;
-    if (n8 > 32 * 32 * 4) {
+    if (!kParts<SRC, FORM> && n8 > 16 * 32 * 4) {
         row_quant_long_kernel<SRC, FORM, BF16><<<static_cast<unsigned>(a.M), 1024, 0, s>>>(a);
         return cudaGetLastError();
     }
     auto warps = [&](int C) { return static_cast<int>((n8 + 32 * C - 1) / (32 * C)); };
+    // Chunks a lane.  One where its warps still fit the GPU at once (512 x 2048 bf16 to INT8: 3.5 us
+    // against 4.5 with two and 5.4 with four).  Then, fp32: two (8192 x 4096 to e4m3: 66.5 us against
+    // 70.9 with four), four where the row would need more than 16 warps; bf16: four (16384 x 4096:
+    // 79.0 against 86.6 with two).
+    constexpr bool any = kParts<SRC, FORM>;  // no limit of warps to a row
+    const int64_t few = static_cast<int64_t>(num_sms) * 48;
     int C = 4;
-    if (warps(1) <= 32 && a.M <= num_sms) C = 1;  // few rows: the shortest chain a lane
-    else if (n8 <= 64 || (warps(2) <= 32 && a.M <= num_sms)) C = 2;
-    const int W = warps(C);
+    if ((any || warps(1) <= 16) && a.M * warps(1) <= few) C = 1;
+    else if ((any || warps(2) <= 16) && (!BF16 || n8 <= 64 || a.M * warps(2) <= few)) C = 2;
+    const int W = any ? 1 : warps(C), parts = any ? warps(C) : 1;
     const int rpc = W >= 8 ? 1 : 8 / W;
-    const int64_t grid = (a.M + rpc - 1) / rpc;
+    if constexpr (SRC == kSrcNorm && BF16) {
+        // Through shared memory where each group of warps has at least three rows of 2048 columns or
+        // more: 16384 x 4096 to e4m3 79.0 -> 73.0 us, to INT8 86.1 -> 77.8, 16384 x 2048 42.0 -> 38.7,
+        // 4096 x 14336 102 -> 70.8; but 16384 x 1024 22.7 -> 23.1, 4096 x 2048 14.6 -> 14.8, and fp32
+        // (which registers already carry at the copy rate) 66.5 -> 68.5.
+        if (C == 4 && a.K >= 2048 && a.M >= static_cast<int64_t>(3 * kStreamBlocks) * num_sms * rpc)
+            return run_stream<FORM>(a, W, rpc, num_sms, s);
+    }
+    const int64_t grid = (a.M * parts + rpc - 1) / rpc;
+    if (grid > 2147483647LL) return cudaErrorInvalidValue;
     switch (C) {
-        case 1: return launch_pdl(row_quant_kernel<SRC, FORM, BF16, 1>, grid, rpc * W * 32, a, W, s);
-        case 2: return launch_pdl(row_quant_kernel<SRC, FORM, BF16, 2>, grid, rpc * W * 32, a, W, s);
-        default: return launch_pdl(row_quant_kernel<SRC, FORM, BF16, 4>, grid, rpc * W * 32, a, W, s);
+        case 1: return launch_pdl(row_quant_kernel<SRC, FORM, BF16, 1>, grid, rpc * W * 32, 0, s, a, W, parts);
+        case 2: return launch_pdl(row_quant_kernel<SRC, FORM, BF16, 2>, grid, rpc * W * 32, 0, s, a, W, parts);
+        default: return launch_pdl(row_quant_kernel<SRC, FORM, BF16, 4>, grid, rpc * W * 32, 0, s, a, W, parts);
     }
 }
 
