@@ -39,7 +39,8 @@
  *     W4A8_ERR_TIMEOUT in a per-device status word and returns early; read it with
  *     w4a8_sync_status().
  *   - The current CUDA device must be an sm_103 GPU; the library holds no state besides
- *     that status word and the one-time device check.
+ *     that status word, the one-time device check and what it asked the driver once about
+ *     its kernels (how many of their CTAs or clusters fit).
  */
 #ifndef W4A8_H_
 #define W4A8_H_
@@ -281,7 +282,8 @@ int w4a8_prefill_linear_host(const float *x_host, const uint8_t *wq, const uint1
  *             w4a8_fp8_linear takes.  K must be a positive multiple of 16 (the last block may be
  *             short); a_q has [M][K] bytes and a_scale [ceil(K/128)][M] floats.
  * Up to the codes every step is one fp32 IEEE operation (swiglu: after t), so the codes of rmsnorm
- * and quant are defined bit for bit; sums of squares are taken in fp32.
+ * and quant are defined bit for bit; sums of squares are taken in fp32, in an order that depends on K
+ * alone: a row's codes and scales are the same in any batch.
  *   - in_dtype: the type of x, residual, residual_out, gate and up, W4A8_IN_F32 or W4A8_IN_BF16
  *     (anything else: W4A8_ERR_ARG).  gamma is fp32 [K], eps finite and > 0 (W4A8_ERR_ARG).
  *   - residual may be NULL; residual_out (the sum h rounded once to in_dtype) may be NULL, be
@@ -315,8 +317,8 @@ int w4a8_quant_fp8(const void *x, int in_dtype, uint8_t *a_q, float *a_scale, in
  * w_scale fp32 [ceil(N/128)][ceil(K/128)] (one per 128 x 128 weights), bias fp32 [N] or NULL;
  * y [M][N] of out_dtype W4A8_OUT_F32 or W4A8_OUT_BF16 (anything else: W4A8_ERR_ARG).  K must be a
  * positive multiple of 16; M and N are any sizes.  Inside a block the tensor cores sum in fp32;
- * the blocks are summed in fp32 in an order that depends only on (M, N, K) and the GPU's SM
- * count, so equal calls give equal bits.  A NaN code (0x7f, 0xff) makes its outputs NaN.
+ * the blocks are summed in fp32 in an order that depends only on (M, N, K) and the GPU, so equal
+ * calls give equal bits.  A NaN code (0x7f, 0xff) makes its outputs NaN.
  * 16-byte alignment: a_q, w_q, y; 4 bytes: a_scale, w_scale, bias. */
 int w4a8_fp8_linear(const uint8_t *a_q, const float *a_scale, const uint8_t *w_q, const float *w_scale,
                     const float *bias, void *y, int out_dtype, int64_t M, int64_t N, int64_t K, void *stream);

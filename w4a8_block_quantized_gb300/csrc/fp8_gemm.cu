@@ -7,14 +7,15 @@
 // fp32 sums in registers, one fma a block and output, y += (sa sw) P_b, while the tensor cores
 // form the next block's product in another accumulator.
 //
-// Orientation: tokens are the MMA's M = 128 operand (TMEM lanes), weight rows its N operand, so a
-// thread owns one token and the factor sa sw is one scalar per thread, block and 128 columns.
-// Operand tiles come straight from the caller's row-major arrays by TMA: 128 rows x 128 columns
+// Two forms.  For large problems tokens are the MMA's M operand (TMEM lanes) and weight rows its N
+// operand: a thread owns one token, and the factor sa sw is one scalar per thread, block and 128
+// columns (pairs of CTAs, below).  For few tokens the roles are swapped.  Operand tiles come straight from the caller's row-major arrays by TMA: 128 rows x 128 columns
 // = one scale block, 128-byte swizzled; rows past M or N and columns past K read as zeros, which
 // add nothing to the products.
 #include "fp8_ptx.cuh"
 #include "ops_internal.h"
 
+#include <atomic>
 #include <cuda_bf16.h>
 
 namespace w4a8 {
@@ -62,8 +63,8 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
 // cluster of `split` CTAs so that every SM has some of it); more tokens, the drain.  Reading one
 // accumulator costs a warp about 700 cycles of waits in a row (barrier, factors, TMEM) however few
 // its columns, so the two sets work on two blocks at a time, each with sums of its own that are
-// added at the end of a tile (one set: 512 x 2048 -> 6144 took 27 us, now @@; 8 x 4096 -> 14336
-// 13.6 us, now @@).  A split sums each output's parts in the order of the ranks, each CTA for its
+// added at the end of a tile (8 x 4096 -> 14336 12.3 us, 13.6 with one set; 512 x 2048 -> 6144 with
+// 128-token tiles 17.5 and 27, of which generic loads were part).  A split sums each output's parts in the order of the ranks, each CTA for its
 // share of the columns, read from the others' shared memory.
 template <int TN_>
 struct Tok {
@@ -337,22 +338,30 @@ __global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __g
         // the accumulators start free
         if (lane == 0)
             for (uint32_t b = set; b < kNBuf && b < total; b += 2) mbar_arrive(&full[b]);
-        uint32_t j0 = 0, js = 0;  // blocks of the tiles done, batches of factors used
+        uint32_t js = 0, odd = 0;  // batches of factors used; the parity of the batch's first block
+        // of this set's next block: its accumulator (and, times 8, its barrier), that barrier's phase, and
+        // the stage (times 8) that its release counts towards
+        uint32_t buf = set, phase = 0, rel = (set + kNBuf) % kStages * 8;
+        const uint32_t bars = smem_u32(tfull), release = smem_u32(full);
         // after a wait gave up this warp waits no more: its sums are then undefined (the status word
         // says so), but it still meets every barrier of the sets and of the cluster
         bool ok = true;
-        for (uint32_t t = first; t < tiles; t += step, j0 += nb) {
+        for (uint32_t t = first; t < tiles; t += step) {
             float y[kCols];
 #pragma unroll
             for (int c = 0; c < kCols; ++c) y[c] = 0.0f;
+#pragma unroll 1
             for (int b0 = 0; b0 < nb; b0 += kChunk, ++js) {
                 if (ok) ok = mbar_poll(&sfull[js & 1u], (js >> 1) & 1, ctl);
+                const int cnt = nb - b0 < kChunk ? nb - b0 : kChunk;
                 const float* f = factors + (js & 1u) * (kChunk * TN) + g * kCols;
-                const int end = nb - b0 < kChunk ? nb - b0 : kChunk;
+                const float* end = f + cnt * TN;
+                f += (set ^ odd) * TN;
+                odd ^= cnt & 1;
 #pragma unroll 1
-                for (int i = (set ^ (j0 + b0)) & 1u; i < end; i += 2) {
-                    const uint32_t j = j0 + b0 + i, buf = j % kNBuf;
-                    if (ok) ok = mbar_poll(&tfull[buf], (j / kNBuf) & 1, ctl);
+                for (; f < end; f += 2 * TN) {
+                    if (__builtin_expect(!mbar_try_wait_long(bars + 8 * buf, phase), 0) && ok)
+                        ok = mbar_wait_on(bars + 8 * buf, phase, ctl);
                     __syncwarp();
                     tc_fence_after();
                     const uint32_t ta = tl + buf * TN;
@@ -366,13 +375,17 @@ __global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __g
 #pragma unroll
                         for (int c = 0; c < kAt; ++c) asm volatile("" : "+r"(v[c]));  // uses stay behind the wait
                         if (c0 + kAt == kCols) {
+                            // released for the block kNBuf later (past the last block: a barrier nobody waits for)
                             tc_fence_before();
                             __syncwarp();
-                            if (lane == 0 && j + kNBuf < total) mbar_arrive(&full[(j + kNBuf) % kStages]);
+                            if (lane == 0) mbar_arrive_on(release + rel);
                         }
 #pragma unroll
-                        for (int c = 0; c < kAt; c += 16) fold16(y + c0 + c, f + i * TN + c0 + c, v + c);
+                        for (int c = 0; c < kAt; c += 16) fold16(y + c0 + c, f + c0 + c, v + c);
                     }
+                    phase ^= buf >> 1;
+                    buf ^= 2u;
+                    rel = rel + 16 >= 8 * kStages ? rel + 16 - 8 * kStages : rel + 16;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sempty[js & 1u]);
@@ -415,18 +428,20 @@ __global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __g
 //               one batch ahead
 //   warps 4-19  drain, 4 lane quarters x 4 runs of 64 columns: a thread holds 64 sums
 //
-// Measured at 8192 x 4096 -> 14336 (bf16 out): 408 us, 2.36 PFLOP/s.  What bounds it is not the tensor
+// Measured at 8192 x 4096 -> 14336 (bf16 out): 341 us, 2.8 PFLOP/s, in short runs; 386 us, 2.5
+// PFLOP/s, in long ones, where the power limit holds the clock near 1.8 GHz.  What bounds it is not the tensor
 // pipe (206 us for the MMAs alone, 258 with the copies and the issue) but what surrounds each block:
 // 32768 fmas a CTA and block (256 cycles of the fp32 pipes, against 512 of the tensor pipe), and the
 // accumulators' way from a commit over the drain back to the issuer, during which their TMEM lies
-// idle (350 us without the fmas).  So:
+// idle (323 us without the fmas).  So:
 //   - four accumulators of 128 columns rather than two of 256: each is handed back as soon as
 //     eight warps of each CTA have read it;
 //   - sixteen draining warps: a warp spends most of a block waiting (barrier, TMEM load), and four
-//     warps a scheduler fill that time with one another's fmas (eight warps of 128 sums: 416 us);
-//   - one wait for an issuer: a stage's barrier counts its copies and the release of the
-//     accumulators that its block overwrites (waits, MMAs and commits of a block cost a thread
-//     about 700 cycles, so two issuers take turns).
+//     warps a scheduler fill that time with one another's fmas (eight warps of 128 sums: 416 us
+//     against 408 at that step);
+//   - the halves of a block are released and waited for one by one: with one wait for both, the
+//     first half's MMAs waited for the second half's drain (350 us, now 341); waits, MMAs and
+//     commits of a block cost a thread about 700 cycles, so two issuers take turns.
 // The outputs leave through a 4 KB staging box per warp and TMA stores (whole lines, rows past M
 // and columns past N cut by the copy) while the tensor cores work on the next tile.
 namespace pair {
@@ -445,10 +460,8 @@ constexpr int kSmemBytes = kOffBar + 256 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 static_assert(kThreads == kSplitThreads, "register split");
 // A wait on parity P returns at once while the phase before P is still open, so all phases of a
-// stage must be waited for by one warp: the two issuers take the even and the odd stages.  And a
-// stage's barrier may count a release only once its previous phase is over: a block's accumulators
-// come free for the block two later, whose stage was last used two blocks before.
-static_assert(kStages % 2 == 0 && kStages > 2, "stages of one issuer; releases after the previous phase");
+// stage must be waited for by one warp: the two issuers take the even and the odd stages.
+static_assert(kStages % 2 == 0, "stages of one issuer");
 }  // namespace pair
 
 // Grouped raster: groups of eight row tiles, the row tile varying fastest inside a group, so the
@@ -530,7 +543,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
     uint64_t* empty = full + kStages;
     uint64_t* tfull = empty + kStages;  // [accumulator]: 2 (block parity) + half of the columns
-    uint64_t* sfull = tfull + 4;
+    static_assert((kOffBar + 2 * kStages * 8) % 64 == 0, "the two parities' barriers differ in one address bit");
+    uint64_t* tempty = tfull + 4;       // the even CTA's, as arrivals go
+    uint64_t* sfull = tempty + 4;
     uint64_t* sempty = sfull + 2;
     uint64_t* drain = sempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
@@ -542,10 +557,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns};
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1 + 2 * kEpiWarps);  // the copies, and both CTAs' epilogue warps
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&tfull[i], 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], kEpiWarps);  // half of the warps of both CTAs
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 32);  // the copying warp's lanes
             mbar_init(&sempty[i], kEpiWarps);
@@ -602,16 +620,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             const uint64_t dw0 = smem_desc(smem_u32(smem + kABytes), 1024, kLayoutSw128);
             const uint32_t d = tmem + par * kBN;
             if (elect_one()) {  // one thread runs the whole loop
-                uint32_t s = par, phase = 0;
+                uint32_t s = par, phase = 0, free = 1;  // waiting for phase 1 of a fresh barrier returns at once
 #pragma unroll 1
                 for (uint32_t j = par; j < total; j += 2) {
-                    if (!mbar_poll(&full[s], phase, ctl)) break;
+                    if (!mbar_poll(&full[s], phase, ctl) || !mbar_poll(&tempty[2 * par], free, ctl)) break;
                     tc_fence_after();
                     const uint64_t o = static_cast<uint64_t>((s * kStageBytes) >> 4);
                     constexpr uint64_t half = (kWRows / 2) * 128 >> 4;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) mma_f8f6f4_pair(d, da0 + o + 2 * k, dw0 + o + 2 * k, idesc, k > 0);
                     mma_commit_pair(&tfull[2 * par]);
+                    if (!mbar_poll(&tempty[2 * par + 1], free, ctl)) break;
+                    tc_fence_after();
+                    free ^= 1u;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_f8f6f4_pair(d + kBN / 2, da0 + o + 2 * k, dw0 + o + half + 2 * k, idesc, k > 0);
@@ -665,11 +686,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * (kBN / 2) + r * 64);
         // their first column in the tile (the run r of an accumulator comes from CTA r's weight rows)
         const int col = r * 128 + h * 64;
-        const uint32_t release = map_rank(&full[0], 0);
-        // the accumulators start free: release those of the first two blocks
-        if (lane == 0)
-            for (uint32_t b = 0; b < 2 && b < total; ++b) mbar_arrive_cluster(release + 8 * b);
-        uint32_t j = 0, js = 0, it = 0;  // blocks drained, batches of scales used, tiles mod 2
+        uint32_t release = map_rank(&tempty[h], 0);
+        uint32_t js = 0, it = 0;  // batches of scales used, tiles mod 2
+        // of the next block: its accumulator's barrier, that barrier's phase, the accumulator, and the
+        // barrier that its release counts towards.  The loop's own instructions matter: with the index
+        // arithmetic, the batch's bounds and the end of the pair's blocks tested for every block, a warp spent 148 instructions on a block's 32 fmas (now
+        // 110; 8192 x 4096 -> 14336 379 -> 344 us).
+        uint32_t bar = smem_u32(&tfull[h]), phase = 0, ta = tl;
+        constexpr uint32_t kBarStep = 16, kTmemStep = kBN;
         for (uint32_t t = first; t < tiles && !*abort_flag; t += step) {
             // the sums start from the bias, which arrives with the tile's first scales
             float y[64];
@@ -687,31 +711,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             }
             it ^= 1;
 #pragma unroll 1
-            for (int b = 0; b < p.nb; ++b, ++j) {
-                const int i = b & (kChunk - 1);
-                const float* sc = scales + (js & 1u) * kScaleFloats;
-                if (i == 0 && b > 0) (void)mbar_poll(&sfull[js & 1u], (js >> 1) & 1, ctl);
-                const float f = sc[i * 128 + q * 32 + lane] * sc[kChunk * 128 + 2 * i + r];
-                if (i == kChunk - 1 || b == p.nb - 1) {
+            for (int b0 = 0; b0 < p.nb; b0 += kChunk) {
+                if (b0 > 0) (void)mbar_poll(&sfull[js & 1u], (js >> 1) & 1, ctl);
+                const float* sa = scales + (js & 1u) * kScaleFloats + q * 32 + lane;
+                const float* sw = scales + (js & 1u) * kScaleFloats + kChunk * 128 + r;
+                const float* end = sw + 2 * (p.nb - b0 < kChunk ? p.nb - b0 : kChunk);
+#pragma unroll 1
+                for (; sw != end; sa += 128, sw += 2) {
+                    const float f = *sa * *sw;
+                    if (__builtin_expect(!mbar_try_wait_long(bar, phase), 0)) (void)mbar_wait_on(bar, phase, ctl);
+                    tc_fence_after();
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(ta, v);
+                    tmem_wait_ld32(v);
+                    fold32(y, f, v);
+                    tmem_ld_32x32b_x32(ta + 32, v);
+                    tmem_wait_ld32(v);
+                    // this warp's columns are read: its part of the accumulator is free for the block two later
+                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sempty[js & 1u]);
-                    ++js;
+                    if (lane == 0) mbar_arrive_cluster(release);
+                    fold32(y + 32, f, v);
+                    phase ^= ta != tl;
+                    bar ^= kBarStep;
+                    ta ^= kTmemStep;
+                    release ^= kBarStep;
                 }
-                (void)mbar_poll(&tfull[2 * (j & 1u) + h], (j >> 1) & 1, ctl);
-                tc_fence_after();
-                const uint32_t ta = tl + (j & 1u) * kBN;
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(ta, v);
-                tmem_wait_ld32(v);
-                fold32(y, f, v);
-                tmem_ld_32x32b_x32(ta + 32, v);
-                tmem_wait_ld32(v);
-                // this warp's columns are read: its part of the accumulators is free for the block
-                // two later
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && j + 2 < total) mbar_arrive_cluster(release + 8 * ((j + 2) % kStages));
-                fold32(y + 32, f, v);
+                if (lane == 0) mbar_arrive(&sempty[js & 1u]);
+                ++js;
             }
             uint32_t tm, tn;
             tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
@@ -813,6 +841,34 @@ cudaError_t launch(Kernel kernel, int smem_bytes, bool* attr_done, int64_t grid,
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// How many clusters of `split` CTAs of the one-CTA kernel run at once (one CTA to an SM, clusters within
+// a GPC, so not num_sms / split: of eight CTAs fewer than 16); asked once.
+template <int TN>
+int tok_clusters(int split) {
+    using T = Tok<TN>;
+    static std::atomic<int> known[9] = {};
+    int n = known[split].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(split));
+    cfg.blockDim = dim3(T::kThreads);
+    cfg.dynamicSmemBytes = T::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(fp8_tok_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, fp8_tok_kernel<TN>, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        return 1;  // not remembered
+    }
+    known[split].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 template <int TN>
 cudaError_t run_tok(Fp8Params& p, const Fp8Args& a, int num_sms, cudaStream_t s) {
     using T = Tok<TN>;
@@ -837,10 +893,10 @@ cudaError_t run_pair(Fp8Params& p, const Fp8Args& a, int num_sms, cudaStream_t s
 }
 
 // Estimated time in us of a form: start, then waves of tiles, each of `blocks` K-blocks and an end.
-// Fitted to measurements (bf16 out, back-to-back launches): 256 x 256 pairs 13.4 us at 512 x 2048 ->
-// 6144 (one wave of 16 blocks), 14.7 at 4096 x 1024 -> 2048 (two of 8), 378 at 8192 x 4096 -> 14336
-// (24 of 32); 128-token tiles 18.1, 21.2; 64-token tiles 16.4, 22.2; and at 256 x 2048 -> 2048 12.3,
-// 10.4 and 7.0.
+// Fitted to measurements (bf16 out, back-to-back launches, us), in the order pairs, 16-, 32-, 64- and
+// 128-token tiles: 512 x 2048 -> 2048 11.0, 12.8, 8.5, 7.0, 10.2; 512 x 8192 -> 2048 31.2, 40.4, 22.8,
+// 16.8, 26.2; 256 x 2048 -> 2048 10.9, 7.7, 5.3, 6.8, 10.0; 512 x 2048 -> 6144 12.3, 31.3, 21.0, 16.0,
+// 17.5; 4096 x 1024 -> 2048 13.7, 45.2, 30.2, 21.5, 20.5; 8 x 4096 -> 14336 22.3, 12.3, 12.7, 17.4, 25.2.
 double form_us(double start, double block, double end, int64_t tiles, int64_t slots, int64_t blocks) {
     const int64_t waves = (tiles + slots - 1) / slots;
     return start + static_cast<double>(waves) * (block * static_cast<double>(blocks) + end);
@@ -850,22 +906,29 @@ double form_us(double start, double block, double end, int64_t tiles, int64_t sl
 struct Form {
     int tn, split;
 };
+int clusters(int tn, int split) {
+    return tn == 16 ? tok_clusters<16>(split) : tn == 32 ? tok_clusters<32>(split) : tn == 64 ? tok_clusters<64>(split)
+                                                                                              : tok_clusters<128>(split);
+}
+
 Form pick_form(int64_t M, int64_t N, int64_t nb, int num_sms) {
     const int64_t n128 = (N + 127) / 128;
     Form best{0, 1};
-    double us = form_us(5.0, 0.43, 1.4, ((M + 255) / 256) * ((N + 255) / 256), num_sms / 2, nb);
+    double us = form_us(1.5, 0.418, 2.7, ((M + 255) / 256) * ((N + 255) / 256), num_sms / 2, nb);
     const int tns[4] = {16, 32, 64, 128};
-    const double block[4] = {0.17, 0.19, 0.23, 0.36}, end[4] = {0.2, 0.3, 0.75, 1.4};
+    const double start[4] = {2.35, 1.9, 2.1, 2.4}, block[4] = {0.153, 0.16, 0.205, 0.335}, end[4] = {0.2, 0.75, 1.33, 2.2};
     for (int i = 0; i < 4; ++i) {
         const int tn = tns[i];
         const int64_t tiles = ((M + tn - 1) / tn) * n128;
-        for (int split = 1; split <= 8 && split <= nb; split *= 2) {
-            // a split has one tile to a cluster, all of them running at once
-            if (split > 1 && tiles * split > num_sms) break;
-            // handing the parts over: 32 x 2048 -> 2048 with 16-token tiles took 5.1, 4.8 and 4.6 us on one,
-            // two and four CTAs a tile, 512 x 6144 -> 1024 with 64-token tiles 13.6 and 10.7 on one and two
-            const double t = form_us(2.4 + (split > 1 ? 0.8 + 0.015 * tn : 0.0), block[i], end[i], tiles, num_sms,
-                                     (nb + split - 1) / split);
+        for (int split = 1, log = 0; split <= 8 && split <= nb; split *= 2, ++log) {
+            // a split has one tile to a cluster, all of them running at once (with eight CTAs a tile and 16
+            // tiles, two waves of clusters, 16 x 6144 -> 2048 took 11.4 us against 6.3 with four)
+            if (split > 1 && (tiles * split > num_sms || tiles > clusters(tn, split))) break;
+            // handing the parts over: 1 x 6144 -> 1024 took 8.9, 6.7, 5.4 and 4.9 us on one, two, four and
+            // eight CTAs a tile, 1 x 1024 -> 1024 3.6, 3.8, 3.7 and 4.1; with 64-token tiles 128 x 6144 ->
+            // 1024 9.7 on two and 8.0 on four
+            const double t = form_us(start[i] + (split > 1 ? 0.4 + 0.32 * log + 0.012 * tn : 0.0), block[i], end[i], tiles,
+                                     num_sms, (nb + split - 1) / split);
             if (t < us) us = t, best = Form{tn, split};
         }
     }

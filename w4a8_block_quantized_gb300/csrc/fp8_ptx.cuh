@@ -7,32 +7,27 @@
 
 namespace w4a8 {
 
-// mbar_wait for waits of a few hundred cycles on a kernel's critical path: one tight loop of up to
-// 2^14 tries, and only after those the abort flag and the clock.
-__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity) {
+// One try that may suspend the thread for up to 100 us, until the phase completes.
+__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-        "mov.u32 n, 0;\n\t"
-        "TRY_%=:\n\t"
+        "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n\t"
-        "@p bra DONE_%=;\n\t"
-        "add.u32 n, n, 1;\n\t"
-        "setp.lt.u32 q, n, 64;\n\t"
-        "@q bra TRY_%=;\n\t"
-        "DONE_%=:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
-    const uint32_t a = smem_u32(bar);
-    if (__builtin_expect(mbar_spin(a, parity), 1)) return true;
+// mbar_wait for waits of a few hundred cycles on a kernel's critical path: up to 64 tries before the
+// abort flag and the clock are looked at.
+__device__ __forceinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, const WaitCtl& ctl) {
     uint64_t t0 = 0;
 #pragma unroll 1
     for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait_long(bar, parity)) return true;
         if (*ctl.abort) return false;
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) t0 = now;
@@ -41,8 +36,16 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, const 
             atomicOr(ctl.status, kStatusTimeout);
             return false;
         }
-        if (mbar_spin(a, parity)) return true;
     }
+}
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
+    const uint32_t a = smem_u32(bar);
+    if (__builtin_expect(mbar_try_wait_long(a, parity), 1)) return true;
+    return mbar_wait_on(a, parity, ctl);
+}
+
+__device__ __forceinline__ void mbar_arrive_on(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // The shared::cluster address of `local` in CTA `rank` of the cluster.
@@ -54,7 +57,7 @@ __device__ __forceinline__ uint32_t map_rank(const void* local, uint32_t rank) {
 
 // An arrival on a barrier of any CTA of the cluster, ordering this thread's accesses for its own
 // CTA only: it announces TMEM reads, which tc_fence_before orders.  (With a release at cluster
-// scope the arrival waited for every load in flight: 20% of the 256 x 256 kernel's rate.)
+// scope each arrival waited for every load in flight: the first pair kernel took 1053 us for 481.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
