@@ -512,9 +512,9 @@ def linear_act(act, wq, w_scale, w_zero, M: int, N: int, K: int, bias=None, y=No
 # expression over cheap attributes; where that fails (or outputs are to be allocated) it goes
 # through the checks that name the offending argument.  Addresses are passed as plain integers,
 # and the current stream is taken as a raw handle.  Measured on the GPU's host, one token through
-# rmsnorm_quant: 13.7 -> 6.3 us a call (the library call itself 2.6; a stream object alone costs 2.8,
+# rmsnorm_quant: 13.7 -> 5.8 us a call (the library call itself 2.6; a stream object alone costs 2.8,
 # the raw handle 0.08).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _handle(index: int, stream) -> int:
@@ -598,30 +598,6 @@ def _e4m3_out(M, K, dev, a_q, a_scale):
     return a_q, a_scale
 
 
-def _fits_int8(index, M, K, a_q, a_scale, rowsum) -> bool:
-    """Whether the three outputs of the INT8 form are given and fit, on the current device `index`."""
-    return a_q.dtype is _I8 and a_scale.dtype is _F32 and rowsum.dtype is _I32 and \
-        a_q.shape == (M, K) and a_scale.shape == (M,) and rowsum.shape == (M, K // 64) and \
-        a_q.get_device() == index and a_scale.get_device() == index and rowsum.get_device() == index and \
-        a_q.is_contiguous() and a_scale.is_contiguous() and rowsum.is_contiguous() and \
-        index == torch.cuda.current_device()
-
-
-def _fits_e4m3(index, M, K, a_q, a_scale) -> bool:
-    """The same for the two outputs of the e4m3 form."""
-    return a_q.dtype is _E8 and a_scale.dtype is _F32 and a_q.shape == (M, K) and \
-        a_scale.shape == ((K + 127) // 128, M) and a_q.get_device() == index and a_scale.get_device() == index and \
-        a_q.is_contiguous() and a_scale.is_contiguous() and index == torch.cuda.current_device()
-
-
-def _fits_norm(index, x, shape, dt, weight, residual, residual_out) -> bool:
-    """Whether all four tensors of a norm with a residual are given and fit."""
-    return weight.dtype is _F32 and residual.dtype is dt and residual_out.dtype is dt and \
-        weight.shape == shape[1:] and residual.shape == shape and residual_out.shape == shape and \
-        weight.get_device() == index and residual.get_device() == index and residual_out.get_device() == index and \
-        x.is_contiguous() and weight.is_contiguous() and residual.is_contiguous() and residual_out.is_contiguous()
-
-
 # what a missing or foreign argument raises in those expressions: the naming checks follow
 _NOT_FITTING = (AttributeError, KeyError, TypeError, ValueError)
 
@@ -639,8 +615,14 @@ def rmsnorm_quant(x, weight, eps, residual=None, residual_out=None, a_q=None, a_
         M, K = shape = x.shape
         index, dt = x.get_device(), x.dtype
         code = _IN_DTYPES[dt]
-        fits = _fits_norm(index, x, shape, dt, weight, residual, residual_out) and \
-            _fits_int8(index, M, K, a_q, a_scale, rowsum)
+        fits = weight.dtype is _F32 and residual.dtype is dt and residual_out.dtype is dt and a_q.dtype is _I8 and \
+            a_scale.dtype is _F32 and rowsum.dtype is _I32 and weight.shape == (K,) and residual.shape == shape and \
+            residual_out.shape == shape and a_q.shape == shape and a_scale.shape == (M,) and \
+            rowsum.shape == (M, K // 64) and weight.get_device() == index and residual.get_device() == index and \
+            residual_out.get_device() == index and a_q.get_device() == index and a_scale.get_device() == index and \
+            rowsum.get_device() == index and x.is_contiguous() and weight.is_contiguous() and \
+            residual.is_contiguous() and residual_out.is_contiguous() and a_q.is_contiguous() and \
+            a_scale.is_contiguous() and rowsum.is_contiguous() and index == _current_device()
     except _NOT_FITTING:
         fits = False
     if not fits:
@@ -648,8 +630,9 @@ def rmsnorm_quant(x, weight, eps, residual=None, residual_out=None, a_q=None, a_
         a_q, a_scale, rowsum = _int8_out(M, K, dev, a_q, a_scale, rowsum)
         index = dev.index
     rc = (_lib or load()).w4a8_rmsnorm_quant(
-        x.data_ptr(), _adr(residual), weight.data_ptr(), eps, code, _adr(residual_out), a_q.data_ptr(),
-        a_scale.data_ptr(), rowsum.data_ptr(), M, K, _raw_stream(index) if stream is None else stream.cuda_stream)
+        x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), eps, code,
+        None if residual_out is None else residual_out.data_ptr(), a_q.data_ptr(), a_scale.data_ptr(),
+        rowsum.data_ptr(), M, K, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "w4a8_rmsnorm_quant")
     return a_q, a_scale, rowsum, residual_out
@@ -673,8 +656,14 @@ def rmsnorm_quant_fp8(x, weight, eps, residual=None, residual_out=None, a_q=None
         M, K = shape = x.shape
         index, dt = x.get_device(), x.dtype
         code = _IN_DTYPES[dt]
-        fits = _fits_norm(index, x, shape, dt, weight, residual, residual_out) and \
-            _fits_e4m3(index, M, K, a_q, a_scale)
+        fits = weight.dtype is _F32 and residual.dtype is dt and residual_out.dtype is dt and a_q.dtype is _E8 and \
+            a_scale.dtype is _F32 and weight.shape == (K,) and residual.shape == shape and \
+            residual_out.shape == shape and a_q.shape == shape and a_scale.shape == ((K + 127) // 128, M) and \
+            weight.get_device() == index and residual.get_device() == index and \
+            residual_out.get_device() == index and a_q.get_device() == index and a_scale.get_device() == index and \
+            x.is_contiguous() and weight.is_contiguous() and residual.is_contiguous() and \
+            residual_out.is_contiguous() and a_q.is_contiguous() and a_scale.is_contiguous() and \
+            index == _current_device()
     except _NOT_FITTING:
         fits = False
     if not fits:
@@ -682,8 +671,8 @@ def rmsnorm_quant_fp8(x, weight, eps, residual=None, residual_out=None, a_q=None
         a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
         index = dev.index
     rc = (_lib or load()).w4a8_rmsnorm_quant_fp8(
-        x.data_ptr(), _adr(residual), weight.data_ptr(), eps, code, _adr(residual_out), a_q.data_ptr(),
-        a_scale.data_ptr(), M, K, _raw_stream(index) if stream is None else stream.cuda_stream)
+        x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), eps, code,
+        None if residual_out is None else residual_out.data_ptr(), a_q.data_ptr(), a_scale.data_ptr(), M, K, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "w4a8_rmsnorm_quant_fp8")
     return a_q, a_scale, residual_out
@@ -718,7 +707,10 @@ def swiglu_quant_fp8(gate, up, a_q=None, a_scale=None, stream=None):
         index, dt, strides = gate.get_device(), gate.dtype, gate.stride()
         code, ld = _IN_DTYPES[dt], strides[0]
         fits = up.shape == shape and up.dtype is dt and up.get_device() == index and up.stride() == strides and \
-            strides[1] == 1 and ld >= K and _fits_e4m3(index, M, K, a_q, a_scale)
+            strides[1] == 1 and ld >= K and a_q.dtype is _E8 and a_scale.dtype is _F32 and a_q.shape == shape and \
+            a_scale.shape == ((K + 127) // 128, M) and a_q.get_device() == index and \
+            a_scale.get_device() == index and a_q.is_contiguous() and a_scale.is_contiguous() and \
+            index == _current_device()
     except _NOT_FITTING:
         fits = False
     if not fits:
@@ -775,14 +767,15 @@ def fp8_linear(a_q, a_scale, w_q, w_scale, bias=None, y=None, out_dtype=None, st
             w_scale.get_device() == index and y.get_device() == index and a_q.is_contiguous() and \
             w_q.is_contiguous() and a_scale.is_contiguous() and w_scale.is_contiguous() and y.is_contiguous() and \
             (bias is None or (bias.dtype is _F32 and bias.shape == (N,) and bias.get_device() == index and
-                              bias.is_contiguous())) and index == torch.cuda.current_device()
+                              bias.is_contiguous())) and index == _current_device()
     except _NOT_FITTING:
         fits = False
     if not fits:
         M, N, K, y = _fp8_in(a_q, a_scale, w_q, w_scale, bias, y, out_dtype)
         index, code = y.get_device(), _OUT_DTYPES[y.dtype]
     rc = (_lib or load()).w4a8_fp8_linear(
-        a_q.data_ptr(), a_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), _adr(bias), y.data_ptr(), code,
+        a_q.data_ptr(), a_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(),
+        None if bias is None else bias.data_ptr(), y.data_ptr(), code,
         M, N, K, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "w4a8_fp8_linear")
