@@ -251,6 +251,13 @@ def test_residual_in_place():
     x2 = x.clone()
     q2, s2, out2 = B().rmsnorm_quant_fp8(x2, w, EPS, residual=res, residual_out=x2)
     assert torch.equal(out2, out0) and torch.equal(q2.view(torch.uint8), q0.view(torch.uint8))
+    # many rows, which come through shared memory ahead of their turn
+    x, res, w = hidden(1, 3700, 4096, BF), normal(2, 3700, 4096).to(BF), 1 + 0.1 * normal(3, 4096)
+    q0, s0, out0 = B().rmsnorm_quant_fp8(x, w, EPS, residual=res)
+    r1, x2 = res.clone(), x.clone()
+    for xx, rr, into in ((x, r1, r1), (x2, res, x2)):
+        q1, s1, out1 = B().rmsnorm_quant_fp8(xx, w, EPS, residual=rr, residual_out=into)
+        assert torch.equal(out0, out1) and torch.equal(s0, s1) and torch.equal(q0.view(torch.uint8), q1.view(torch.uint8))
     # a row past the register-resident depth
     x, res, w = hidden(1, 3, 33024, F32), normal(2, 3, 33024), 1 + 0.1 * normal(3, 33024)
     q0, _, out0 = B().rmsnorm_quant_fp8(x, w, EPS, residual=res)
@@ -395,10 +402,11 @@ def test_other_streams_and_tapes():
     tape.free()
 
 
-def test_back_to_back_calls_keep_their_order():
+@pytest.mark.parametrize("M,K", [(40, 1024), (700, 1024), (2600, 2048), (7400, 2048)])
+def test_back_to_back_calls_keep_their_order(M, K):
     """A chain of dependent calls without a wait between them, many times over: each kernel may start
-    early (programmatic launch) but reads only finished results."""
-    M, K = 40, 1024
+    early (programmatic launch) but reads only finished results.  The sizes reach every form of the
+    linear and both kernels of the norm."""
     w = 1 + 0.1 * normal(3, K)
     _, _, wq, sw, _ = operands(3, 1, K, K)
     def chain():
