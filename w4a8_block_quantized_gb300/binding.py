@@ -672,7 +672,8 @@ def rmsnorm_quant_fp8(x, weight, eps, residual=None, residual_out=None, a_q=None
         index = dev.index
     rc = (_lib or load()).w4a8_rmsnorm_quant_fp8(
         x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), eps, code,
-        None if residual_out is None else residual_out.data_ptr(), a_q.data_ptr(), a_scale.data_ptr(), M, K, _raw_stream(index) if stream is None else stream.cuda_stream)
+        None if residual_out is None else residual_out.data_ptr(), a_q.data_ptr(), a_scale.data_ptr(), M, K,
+        _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "w4a8_rmsnorm_quant_fp8")
     return a_q, a_scale, residual_out

@@ -9,9 +9,9 @@
 //
 // Two forms.  For large problems tokens are the MMA's M operand (TMEM lanes) and weight rows its N
 // operand: a thread owns one token, and the factor sa sw is one scalar per thread, block and 128
-// columns (pairs of CTAs, below).  For few tokens the roles are swapped.  Operand tiles come straight from the caller's row-major arrays by TMA: 128 rows x 128 columns
-// = one scale block, 128-byte swizzled; rows past M or N and columns past K read as zeros, which
-// add nothing to the products.
+// columns (pairs of CTAs, below).  For few tokens the roles are swapped.  Operand tiles come straight
+// from the caller's row-major arrays by TMA, 128 columns = one scale block wide, 128-byte swizzled;
+// rows past M or N and columns past K read as zeros, which add nothing to the products.
 #include "fp8_ptx.cuh"
 #include "ops_internal.h"
 
@@ -64,8 +64,8 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
 // accumulator costs a warp about 700 cycles of waits in a row (barrier, factors, TMEM) however few
 // its columns, so the two sets work on two blocks at a time, each with sums of its own that are
 // added at the end of a tile (8 x 4096 -> 14336 12.3 us, 13.6 with one set; 512 x 2048 -> 6144 with
-// 128-token tiles 17.5 and 27, of which generic loads were part).  A split sums each output's parts in the order of the ranks, each CTA for its
-// share of the columns, read from the others' shared memory.
+// 128-token tiles 17.5 and 27, of which generic loads were part).  A split sums each output's parts in
+// the order of the ranks, each CTA for its share of the columns, read from the others' shared memory.
 template <int TN_>
 struct Tok {
     static constexpr int TN = TN_;
@@ -77,15 +77,16 @@ struct Tok {
     static constexpr int kWBytes = 128 * 128, kStageBytes = kWBytes + TN * 128;
     static constexpr uint32_t kTmemCols = TN * kNBuf;
     static constexpr int kChunk = 8;                    // blocks per batch of factors
-    static constexpr int kOffPart = kStages * kStageBytes;  // the odd set's sums [column][weight row]
+    static constexpr int kOffPart = kStages * kStageBytes;  // the sets' exchange area [column][weight row]
     static constexpr int kOffScale = kOffPart + TN * 512;
     static constexpr int kScaleBytes = kChunk * TN * 4;
     static constexpr int kRawFloats = kChunk * TN + kChunk;  // the scales they are formed from: sa, then sw
     static constexpr int kOffRaw = kOffScale + 2 * kScaleBytes;
     static constexpr int kOffBar = kOffRaw + 2 * kRawFloats * 4;
     static constexpr int kSmemBytes = kOffBar + 512 + 1024;
-    // Register split of the 640-thread form with 64 sums a thread (see the pair form).
+    // The 640-thread form with 64 sums a thread re-splits its registers.
     static constexpr bool kResplit = kCols == 64;
+    static_assert(!kResplit || kThreads == kSplitThreads, "register split");
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
     static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 512, "TMEM allocation");
     // Each stage and each accumulator has one issuer and one set at every phase (their counts are
@@ -161,7 +162,8 @@ __device__ __forceinline__ void store_share(const Fp8Params& p, const float* sum
         for (uint32_t k = 0; k < split; ++k) {
             float r[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[e] = c + e * G < c1 ? ld_shared_cluster_f32(sums + (c + e * G) * 128 + row, k) : 0.0f;
+            for (int e = 0; e < 8; ++e)
+                r[e] = c + e * G < c1 ? ld_shared_cluster_f32(sums + (c + e * G) * 128 + row, k) : 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += r[e];
         }
@@ -229,105 +231,105 @@ __global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __g
     const uint32_t total = tiles > first ? ((tiles - 1 - first) / step + 1) * static_cast<uint32_t>(nb) : 0u;
 
     if (warp < 4) {
-    if constexpr (T::kResplit) regs_dec<kRegsLow>();
-    if (warp == 0) {
-        if (lane == 0) {
-            uint32_t j = 0, issued = 0;
-            bool ok = true;
-            for (uint32_t t = first; ok && t < tiles; t += step) {
-                const int m0 = static_cast<int>(t % p.tiles_m) * TN, n0 = static_cast<int>(t / p.tiles_m) * 128;
+        if constexpr (T::kResplit) regs_dec<kRegsLow>();
+        if (warp == 0) {
+            if (lane == 0) {
+                uint32_t j = 0, issued = 0;
+                bool ok = true;
+                for (uint32_t t = first; ok && t < tiles; t += step) {
+                    const int m0 = static_cast<int>(t % p.tiles_m) * TN, n0 = static_cast<int>(t / p.tiles_m) * 128;
 #pragma unroll 1
-                for (int b = 0; b < nb; ++b, ++j) {
-                    const uint32_t s = j % kStages, k = j / kStages;
-                    if (k > 0 && !mbar_poll(&empty[s], (k - 1) & 1, ctl)) {
-                        ok = false;
-                        break;
+                    for (int b = 0; b < nb; ++b, ++j) {
+                        const uint32_t s = j % kStages, k = j / kStages;
+                        if (k > 0 && !mbar_poll(&empty[s], (k - 1) & 1, ctl)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&full[s], kStageBytes);
+                        tma_load_2d(smem + s * kStageBytes, &p.wmap, (kb0 + b) * 128, n0, &full[s]);
+                        tma_load_2d(smem + s * kStageBytes + T::kWBytes, &p.amap, (kb0 + b) * 128, m0, &full[s]);
+                        issued = j + 1;
                     }
-                    mbar_arrive_expect_tx(&full[s], kStageBytes);
-                    tma_load_2d(smem + s * kStageBytes, &p.wmap, (kb0 + b) * 128, n0, &full[s]);
-                    tma_load_2d(smem + s * kStageBytes + T::kWBytes, &p.amap, (kb0 + b) * 128, m0, &full[s]);
-                    issued = j + 1;
                 }
+                if (*abort_flag)  // let every copy already issued land before the CTA exits
+                    for (uint32_t q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
+                        drain_wait(&full[q % kStages], (q / kStages) & 1, 10000000ull);
             }
-            if (*abort_flag)  // let every copy already issued land before the CTA exits
-                for (uint32_t q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
-                    drain_wait(&full[q % kStages], (q / kStages) & 1, 10000000ull);
-        }
-        __syncwarp();
-    } else if (warp <= 2) {
-        constexpr uint32_t idesc = idesc_e4m3_f32(128, TN);
-        const uint32_t par = warp - 1;
-        const uint64_t dw0 = smem_desc(smem_u32(smem), 1024, kLayoutSw128);
-        const uint64_t dt0 = smem_desc(smem_u32(smem + T::kWBytes), 1024, kLayoutSw128);
-        // one thread runs the whole loop: elected anew for every block, a warp lost 100 cycles a block
-        if (elect_one()) {
-            uint32_t s = par, phase = 0, buf = par;
+            __syncwarp();
+        } else if (warp <= 2) {
+            constexpr uint32_t idesc = idesc_e4m3_f32(128, TN);
+            const uint32_t par = warp - 1;
+            const uint64_t dw0 = smem_desc(smem_u32(smem), 1024, kLayoutSw128);
+            const uint64_t dt0 = smem_desc(smem_u32(smem + T::kWBytes), 1024, kLayoutSw128);
+            if (elect_one()) {  // one thread runs the whole loop
+                uint32_t s = par, phase = 0, buf = par;
 #pragma unroll 1
-            for (uint32_t j = par; j < total; j += 2) {
-                if (!mbar_poll(&full[s], phase, ctl)) break;
-                tc_fence_after();
-                const uint64_t o = static_cast<uint64_t>((s * kStageBytes) >> 4);
+                for (uint32_t j = par; j < total; j += 2) {
+                    if (!mbar_poll(&full[s], phase, ctl)) break;
+                    tc_fence_after();
+                    const uint64_t o = static_cast<uint64_t>((s * kStageBytes) >> 4);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_f8f6f4(tmem + buf * TN, dw0 + o + 2 * k, dt0 + o + 2 * k, idesc, k > 0);
-                mma_commit(&tfull[buf]);
-                mma_commit(&empty[s]);
-                buf ^= 2u;
-                if ((s += 2) >= kStages) s -= kStages, phase ^= 1u;
-            }
-            mma_commit(&drain[par]);
-        }
-        __syncwarp();
-        drain_wait(&drain[par], 0, 100000000ull);
-    } else {
-        // the scales of a batch are copied while the factors of the one before are formed (a loader
-        // that waited for its loads held the drain up: 512 x 2048 -> 6144 took 30 us with one)
-        uint32_t j = 0;  // batches
-        uint32_t tn = first, bn = 0;  // the next batch to copy: tile, block
-        auto copy = [&](uint32_t buf) {
-            if (tn < tiles && nb > 0) {
-                const int64_t m0 = static_cast<int64_t>(tn % p.tiles_m) * TN;
-                const float* sw = p.sw + static_cast<int64_t>(tn / p.tiles_m) * p.nb + kb0 + bn;
-                const float* sa = p.sa + (kb0 + bn) * p.M + m0;
-                const int last = p.M - m0 < TN ? static_cast<int>(p.M - m0) - 1 : TN - 1;  // columns past M: unused
-                const int cnt = nb - static_cast<int>(bn) < kChunk ? nb - static_cast<int>(bn) : kChunk;
-                float* d = raw + buf * T::kRawFloats;
-#pragma unroll 1
-                for (int c = lane; c < TN; c += 32) {
-                    const float* src = sa + (c < last ? c : last);
-#pragma unroll 1
-                    for (int k = 0; k < cnt; ++k, src += p.M) cp_async4(d + k * TN + c, src);
+                    for (int k = 0; k < 4; ++k)
+                        mma_f8f6f4(tmem + buf * TN, dw0 + o + 2 * k, dt0 + o + 2 * k, idesc, k > 0);
+                    mma_commit(&tfull[buf]);
+                    mma_commit(&empty[s]);
+                    buf ^= 2u;
+                    if ((s += 2) >= kStages) s -= kStages, phase ^= 1u;
                 }
-                if (lane < cnt) cp_async4(d + kChunk * TN + lane, sw + lane);
-                bn += kChunk;
-                if (static_cast<int>(bn) >= nb) bn = 0, tn += step;
+                mma_commit(&drain[par]);
             }
-            cp_async_commit();
-        };
-        copy(0);
-        for (uint32_t t = first; t < tiles && !*abort_flag; t += step) {
-            for (int b0 = 0; b0 < nb; b0 += kChunk, ++j) {
-                const uint32_t buf = j & 1u, u = j >> 1;
-                const int cnt = nb - b0 < kChunk ? nb - b0 : kChunk;
-                copy(buf ^ 1u);
-                cp_async_wait<1>();
-                __syncwarp();
-                if (u > 0) (void)mbar_poll(&sempty[buf], (u - 1) & 1, ctl);
-                float* d = factors + buf * (kChunk * TN);
-                const float* r = raw + buf * T::kRawFloats;
+            __syncwarp();
+            drain_wait(&drain[par], 0, 100000000ull);
+        } else {
+            // the scales of a batch are copied while the factors of the one before are formed (a loader
+            // that waited for its loads held the drain up: 512 x 2048 -> 6144 took 30 us with one)
+            uint32_t j = 0;  // batches
+            uint32_t tn = first, bn = 0;  // the next batch to copy: tile, block
+            auto copy = [&](uint32_t buf) {
+                if (tn < tiles && nb > 0) {
+                    const int64_t m0 = static_cast<int64_t>(tn % p.tiles_m) * TN;
+                    const float* sw = p.sw + static_cast<int64_t>(tn / p.tiles_m) * p.nb + kb0 + bn;
+                    const float* sa = p.sa + (kb0 + bn) * p.M + m0;
+                    const int last = p.M - m0 < TN ? static_cast<int>(p.M - m0) - 1 : TN - 1;  // columns past M: unused
+                    const int cnt = nb - static_cast<int>(bn) < kChunk ? nb - static_cast<int>(bn) : kChunk;
+                    float* d = raw + buf * T::kRawFloats;
 #pragma unroll 1
-                for (int k = 0; k < cnt; ++k) {
-                    const float w = r[kChunk * TN + k];
+                    for (int c = lane; c < TN; c += 32) {
+                        const float* src = sa + (c < last ? c : last);
+#pragma unroll 1
+                        for (int k = 0; k < cnt; ++k, src += p.M) cp_async4(d + k * TN + c, src);
+                    }
+                    if (lane < cnt) cp_async4(d + kChunk * TN + lane, sw + lane);
+                    bn += kChunk;
+                    if (static_cast<int>(bn) >= nb) bn = 0, tn += step;
+                }
+                cp_async_commit();
+            };
+            copy(0);
+            for (uint32_t t = first; t < tiles && !*abort_flag; t += step) {
+                for (int b0 = 0; b0 < nb; b0 += kChunk, ++j) {
+                    const uint32_t buf = j & 1u, u = j >> 1;
+                    const int cnt = nb - b0 < kChunk ? nb - b0 : kChunk;
+                    copy(buf ^ 1u);
+                    cp_async_wait<1>();
+                    __syncwarp();
+                    if (u > 0) (void)mbar_poll(&sempty[buf], (u - 1) & 1, ctl);
+                    float* d = factors + buf * (kChunk * TN);
+                    const float* r = raw + buf * T::kRawFloats;
+#pragma unroll 1
+                    for (int k = 0; k < cnt; ++k) {
+                        const float w = r[kChunk * TN + k];
 #pragma unroll
-                    for (int c = 0; c < TN; c += 32)
-                        if (TN >= 32 || lane < TN) d[k * TN + c + lane] = r[k * TN + c + lane] * w;
+                        for (int c = 0; c < TN; c += 32)
+                            if (TN >= 32 || lane < TN) d[k * TN + c + lane] = r[k * TN + c + lane] * w;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sfull[buf]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sfull[buf]);
             }
+            cp_async_wait<0>();
+            __syncwarp();
         }
-        cp_async_wait<0>();
-        __syncwarp();
-    }
     } else {
         if constexpr (T::kResplit) regs_inc<kRegsHigh>();
         // set, lane quarter, column group
@@ -690,8 +692,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         uint32_t js = 0, it = 0;  // batches of scales used, tiles mod 2
         // of the next block: its accumulator's barrier, that barrier's phase, the accumulator, and the
         // barrier that its release counts towards.  The loop's own instructions matter: with the index
-        // arithmetic, the batch's bounds and the end of the pair's blocks tested for every block, a warp spent 148 instructions on a block's 32 fmas (now
-        // 110; 8192 x 4096 -> 14336 379 -> 344 us).
+        // arithmetic, the batch's bounds and the end of the pair's blocks tested for every block, a warp
+        // spent 148 instructions on a block's 32 fmas (now 110; 8192 x 4096 -> 14336 379 -> 344 us).
         uint32_t bar = smem_u32(&tfull[h]), phase = 0, ta = tl;
         constexpr uint32_t kBarStep = 16, kTmemStep = kBN;
         for (uint32_t t = first; t < tiles && !*abort_flag; t += step) {
@@ -860,7 +862,8 @@ int tok_clusters(int split) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(fp8_tok_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess ||
+    if (cudaFuncSetAttribute(fp8_tok_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) !=
+            cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, fp8_tok_kernel<TN>, &cfg) != cudaSuccess || n < 1) {
         (void)cudaGetLastError();
         return 1;  // not remembered

@@ -18,8 +18,8 @@
 // 8-byte stores of codes), straight from memory or, for many rows, through a ring of rows in shared
 // memory.  Rows past 16 warps x 4 chunks take the looping kernel, which reads twice (the second time
 // from L2).  What bounds it: HBM bytes for many rows (16384 x 4096 bf16 norm to e4m3: 73 us, 6.4 TB/s,
-// 96% of the copy rate; 8192 x 14336 bf16 gated activation 90 us, 6.6 TB/s, 99%), the latency of one load -> reduce -> store chain
-// for few (1 x 4096: 2.5 us).
+// 96% of the copy rate; 8192 x 14336 bf16 gated activation 90 us, 6.6 TB/s, 98%), the latency of one
+// load -> reduce -> store chain for few (1 x 4096: 2.5 us).
 #include "ops_internal.h"
 #include "quant_math.cuh"
 #include "sm103_ptx.cuh"
@@ -312,8 +312,8 @@ __device__ __forceinline__ void row_reduce(float& amax, const float (&sum)[C], f
 }
 
 // One row (`row`: it exists), or its part from chunk `base` on, held by W warps, this one the wg-th:
-// chunk base + (i W + wg) 32 + lane is input(i), its gamma gamma(i), i < C.  After `read()` the inputs are in registers (of every lane
-// of this warp; the row's other warps meet in the reduction).
+// chunk base + (i W + wg) 32 + lane is input(i), its gamma gamma(i), i < C.  After `read()` the inputs
+// are in registers (of every lane of this warp; the row's other warps meet in the reduction).
 template <int SRC, int FORM, bool BF16, int C, typename Input, typename Gamma, typename Read>
 __device__ __forceinline__ void work_row(const RowArgs& a, int64_t m, bool row, int64_t base, int W, int wg, int lane,
                                          float* red, int bar, Input&& input, Gamma&& gamma, Read&& read) {
