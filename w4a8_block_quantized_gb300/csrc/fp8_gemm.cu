@@ -39,6 +39,7 @@ struct Fp8Params {
     int split;  // CTAs (a cluster) sharing a tile's K
     uint32_t* status;
     uint64_t wait_limit_ns;
+    uint32_t copy_blocks;  // a CTA's copies stop before this block (none: the last one's number is smaller)
 };
 
 // Bounded wait that ignores the abort flag: used while unwinding, so that copies and MMAs in
@@ -49,6 +50,19 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
     while (!mbar_try_wait(a, parity)) {
         if (globaltimer_ns() - t0 > limit_ns) return;
     }
+}
+
+// What follows a wait that gave up.  The flag that says so can rise between two lanes' reads of it, so
+// no lane leaves a loop on its own: a warp decides for all its lanes together (all_ok), because the
+// instructions ahead (TMEM loads, named barriers, __syncwarp) want the whole warp.
+__device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+// The copies of blocks 0 .. issued - 1 that may still be in flight land (for a bounded time) before the
+// CTA leaves; for one thread, once every role has ended.
+template <int STAGES>
+__device__ __forceinline__ void land_copies(uint64_t* full, uint32_t issued) {
+    for (uint32_t q = issued > STAGES ? issued - STAGES : 0; q < issued; ++q)
+        drain_wait(&full[q % STAGES], (q / STAGES) & 1, 10000000ull);
 }
 
 // ---------------------------------------------------------------- one CTA, weights on the lanes
@@ -121,6 +135,7 @@ template <int C, int K0, int THREADS>
 __device__ __forceinline__ void finish_cols(const Fp8Params& p, float* part, const float (&y)[C], int64_t m0, int64_t n,
                                             bool split, bool first) {
     constexpr int G0 = C / 2 - K0;  // the half it hands over
+    __syncwarp();  // named barriers take whole warps
     if (!first) named_bar_sync(1, THREADS);  // the last tile's have been read
 #pragma unroll
     for (int c = 0; c < C / 2; ++c) part[(G0 + c) * 128] = y[G0 + c];
@@ -194,6 +209,7 @@ __global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __g
     uint64_t* drain = sempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    uint32_t* issued = tmem_slot + 2;  // blocks whose copies were issued; read after an abort
     float* factors = reinterpret_cast<float*>(smem + T::kOffScale);
     float* raw = reinterpret_cast<float*>(smem + T::kOffRaw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -234,26 +250,23 @@ __global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __g
         if constexpr (T::kResplit) regs_dec<kRegsLow>();
         if (warp == 0) {
             if (lane == 0) {
-                uint32_t j = 0, issued = 0;
+                uint32_t j = 0;
                 bool ok = true;
                 for (uint32_t t = first; ok && t < tiles; t += step) {
                     const int m0 = static_cast<int>(t % p.tiles_m) * TN, n0 = static_cast<int>(t / p.tiles_m) * 128;
 #pragma unroll 1
                     for (int b = 0; b < nb; ++b, ++j) {
                         const uint32_t s = j % kStages, k = j / kStages;
-                        if (k > 0 && !mbar_poll(&empty[s], (k - 1) & 1, ctl)) {
+                        if (j >= p.copy_blocks || (k > 0 && !mbar_poll(&empty[s], (k - 1) & 1, ctl))) {
                             ok = false;
                             break;
                         }
                         mbar_arrive_expect_tx(&full[s], kStageBytes);
                         tma_load_2d(smem + s * kStageBytes, &p.wmap, (kb0 + b) * 128, n0, &full[s]);
                         tma_load_2d(smem + s * kStageBytes + T::kWBytes, &p.amap, (kb0 + b) * 128, m0, &full[s]);
-                        issued = j + 1;
                     }
                 }
-                if (*abort_flag)  // let every copy already issued land before the CTA exits
-                    for (uint32_t q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
-                        drain_wait(&full[q % kStages], (q / kStages) & 1, 10000000ull);
+                *issued = j;
             }
             __syncwarp();
         } else if (warp <= 2) {
@@ -306,14 +319,15 @@ __global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __g
                 cp_async_commit();
             };
             copy(0);
-            for (uint32_t t = first; t < tiles && !*abort_flag; t += step) {
+            bool ok = true;
+            for (uint32_t t = first; ok && t < tiles; t += step) {
                 for (int b0 = 0; b0 < nb; b0 += kChunk, ++j) {
                     const uint32_t buf = j & 1u, u = j >> 1;
                     const int cnt = nb - b0 < kChunk ? nb - b0 : kChunk;
                     copy(buf ^ 1u);
                     cp_async_wait<1>();
                     __syncwarp();
-                    if (u > 0) (void)mbar_poll(&sempty[buf], (u - 1) & 1, ctl);
+                    if (u > 0 && !(ok = all_ok(mbar_poll(&sempty[buf], (u - 1) & 1, ctl)))) break;
                     float* d = factors + buf * (kChunk * TN);
                     const float* r = raw + buf * T::kRawFloats;
 #pragma unroll 1
@@ -362,7 +376,7 @@ __global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __g
                 odd ^= cnt & 1;
 #pragma unroll 1
                 for (; f < end; f += 2 * TN) {
-                    if (__builtin_expect(!mbar_try_wait_long(bars + 8 * buf, phase), 0) && ok)
+                    if (ok && __builtin_expect(!mbar_try_wait_long(bars + 8 * buf, phase), 0))
                         ok = mbar_wait_on(bars + 8 * buf, phase, ctl);
                     __syncwarp();
                     tc_fence_after();
@@ -408,8 +422,10 @@ __global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __g
                                                static_cast<int>(rank) * share, (static_cast<int>(rank) + 1) * share, split);
         cluster_sync_all();  // no CTA leaves while another may still read its sums
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) land_copies<kStages>(full, *issued);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, T::kTmemCols);
@@ -552,6 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     uint64_t* drain = sempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    uint32_t* issued = tmem_slot + 2;  // blocks whose copies were issued; read after an abort
     float* scales = reinterpret_cast<float*>(smem + kOffScale);
     float* biases = reinterpret_cast<float*>(smem + kOffBias);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -590,7 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     if (warp < 4) {
         regs_dec<kRegsLow>();
         if (warp == 0 && lane == 0) {
-            uint32_t j = 0, issued = 0;
+            uint32_t j = 0;
             bool ok = true;
             for (uint32_t t = first; ok && t < tiles; t += step) {
                 uint32_t tm, tn;
@@ -599,21 +616,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 #pragma unroll 1
                 for (int b = 0; b < p.nb; ++b, ++j) {
                     const uint32_t s = j % kStages, k = j / kStages;
-                    if (k > 0 && !mbar_poll(&empty[s], (k - 1) & 1, ctl)) {
+                    if (j >= p.copy_blocks || (k > 0 && !mbar_poll(&empty[s], (k - 1) & 1, ctl))) {
                         ok = false;
                         break;
                     }
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
                     tma_load_2d_pair(smem + s * kStageBytes, &p.amap, b * 128, m0, &full[s]);
                     tma_load_2d_pair(smem + s * kStageBytes + kABytes, &p.wmap, b * 128, n0, &full[s]);
-                    issued = j + 1;
                 }
             }
-            // after a wait gave up: both CTAs' copies land on the even CTA's barriers, which it
-            // watches (for a bounded time) before the cluster's last barrier lets either leave
-            if (*abort_flag && rank == 0)
-                for (uint32_t q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
-                    drain_wait(&full[q % kStages], (q / kStages) & 1, 10000000ull);
+            *issued = j;
         } else if ((warp == 1 || warp == 2) && rank == 0) {
             // An accumulator's 128 columns: 64 weight rows of each CTA's box.
             constexpr uint32_t idesc = idesc_e4m3_f32(kBM, kBN / 2);
@@ -648,7 +660,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             drain_wait(&drain[par], 0, 100000000ull);
         } else if (warp == 3) {
             uint32_t j = 0, i = 0;  // batches staged, tiles
-            for (uint32_t t = first; t < tiles && !*abort_flag; t += step, ++i) {
+            bool ok = true;
+            for (uint32_t t = first; ok && t < tiles; t += step, ++i) {
                 uint32_t tm, tn;
                 tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
                 const int64_t m0 = static_cast<int64_t>(tm) * kBM + rank * 128;
@@ -657,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                 for (int b0 = 0; b0 < p.nb; b0 += kChunk, ++j) {
                     const uint32_t buf = j & 1u, u = j >> 1;
                     const int cnt = p.nb - b0 < kChunk ? p.nb - b0 : kChunk;
-                    if (u > 0) (void)mbar_poll(&sempty[buf], (u - 1) & 1, ctl);
+                    if (u > 0 && !(ok = all_ok(mbar_poll(&sempty[buf], (u - 1) & 1, ctl)))) break;
                     float* d = scales + buf * kScaleFloats;
 #pragma unroll 1
                     for (int e = lane; e < 128; e += 32) {
@@ -679,6 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                     cp_async_arrive(&sfull[buf]);
                 }
             }
+            cp_async_wait_all();
         }
         __syncwarp();
     } else {
@@ -696,7 +710,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         // spent 148 instructions on a block's 32 fmas (now 110; 8192 x 4096 -> 14336 379 -> 344 us).
         uint32_t bar = smem_u32(&tfull[h]), phase = 0, ta = tl;
         constexpr uint32_t kBarStep = 16, kTmemStep = kBN;
-        for (uint32_t t = first; t < tiles && !*abort_flag; t += step) {
+        // after a wait gave up the warp ends with its tile, whose sums are undefined (the status word says so)
+        for (uint32_t t = first; t < tiles && all_ok(!*abort_flag); t += step) {
             // the sums start from the bias, which arrives with the tile's first scales
             float y[64];
             (void)mbar_poll(&sfull[js & 1u], (js >> 1) & 1, ctl);
@@ -713,7 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             }
             it ^= 1;
 #pragma unroll 1
-            for (int b0 = 0; b0 < p.nb; b0 += kChunk) {
+            for (int b0 = 0; b0 < p.nb && all_ok(!*abort_flag); b0 += kChunk) {
                 if (b0 > 0) (void)mbar_poll(&sfull[js & 1u], (js >> 1) & 1, ctl);
                 const float* sa = scales + (js & 1u) * kScaleFloats + q * 32 + lane;
                 const float* sw = scales + (js & 1u) * kScaleFloats + kChunk * 128 + r;
@@ -722,6 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                 for (; sw != end; sa += 128, sw += 2) {
                     const float f = *sa * *sw;
                     if (__builtin_expect(!mbar_try_wait_long(bar, phase), 0)) (void)mbar_wait_on(bar, phase, ctl);
+                    __syncwarp();  // the TMEM loads take the whole warp
                     tc_fence_after();
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(ta, v);
@@ -765,6 +781,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) {
+        // both CTAs' copies land on the even CTA's barriers; the odd one has only the time to go by
+        if (rank == 0) land_copies<kStages>(full, *issued);
+        else drain_wait(&full[0], 0, 10000000ull);
+    }
     cluster_sync_all();  // neither CTA leaves while the other may still signal it or read its memory
     if (warp == 1) {
         tc_fence_after();
@@ -938,10 +959,7 @@ Form pick_form(int64_t M, int64_t N, int64_t nb, int num_sms) {
     return best;
 }
 
-}  // namespace
-
-cudaError_t launch_fp8_linear(const Fp8Args& a, int num_sms, cudaStream_t s) {
-    if (num_sms < 1) return cudaErrorInvalidValue;
+cudaError_t launch_form(const Fp8Args& a, Form f, int num_sms, cudaStream_t s) {
     Fp8Params p;
     p.sa = a.sa;
     p.sw = a.sw;
@@ -952,10 +970,10 @@ cudaError_t launch_fp8_linear(const Fp8Args& a, int num_sms, cudaStream_t s) {
     p.M = a.M;
     p.N = a.N;
     p.nb = static_cast<int>((a.K + kGroup8 - 1) / kGroup8);
+    p.split = f.split;
     p.status = a.status;
     p.wait_limit_ns = a.wait_limit_ns;
-    const Form f = pick_form(a.M, a.N, p.nb, num_sms);
-    p.split = f.split;
+    p.copy_blocks = a.copy_blocks;
     switch (f.tn) {
         case 0: return run_pair(p, a, num_sms, s);
         case 16: return run_tok<16>(p, a, num_sms, s);
@@ -963,6 +981,13 @@ cudaError_t launch_fp8_linear(const Fp8Args& a, int num_sms, cudaStream_t s) {
         case 64: return run_tok<64>(p, a, num_sms, s);
         default: return run_tok<128>(p, a, num_sms, s);
     }
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_linear(const Fp8Args& a, int num_sms, cudaStream_t s) {
+    if (num_sms < 1) return cudaErrorInvalidValue;
+    return launch_form(a, pick_form(a.M, a.N, (a.K + kGroup8 - 1) / kGroup8, num_sms), num_sms, s);
 }
 
 }  // namespace w4a8

@@ -58,6 +58,7 @@ struct Fp8Args {
     int64_t M = 0, N = 0, K = 0;
     uint32_t* status = nullptr;
     uint64_t wait_limit_ns = 1000000000ull;
+    uint32_t copy_blocks = 0xffffffffu;  // fewer than a CTA has: its waits run out (tests of the bounded waits)
 };
 
 cudaError_t launch_fp8_linear(const Fp8Args& a, int num_sms, cudaStream_t s);

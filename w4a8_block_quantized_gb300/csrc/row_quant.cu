@@ -303,6 +303,7 @@ __device__ __forceinline__ void row_reduce(float& amax, const float (&sum)[C], f
     } else {
         if (MAX && lane == 0) red[wg] = amax;
         if (SUM && (lane & (32 / C - 1)) == 0) red[W + slot<C, 16>(lane) * W + wg] = seg;
+        __syncwarp();  // named barriers take whole warps
         named_bar_sync(bar, W * 32);
         if (MAX) amax = reduce<1, 16>({lane < W ? red[lane] : 0.0f}, lane, Max());
         if (SUM)
