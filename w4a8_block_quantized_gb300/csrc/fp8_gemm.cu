@@ -786,6 +786,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         if (rank == 0) land_copies<kStages>(full, *issued);
         else drain_wait(&full[0], 0, 10000000ull);
     }
+    // the issuers' last commits arrive on this CTA's barriers too: it may not leave before they have
+    if (rank == 1 && threadIdx.x < 2) drain_wait(&drain[threadIdx.x], 0, 100000000ull);
     cluster_sync_all();  // neither CTA leaves while the other may still signal it or read its memory
     if (warp == 1) {
         tc_fence_after();
