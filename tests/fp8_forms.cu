@@ -8,7 +8,20 @@ using namespace w4a8;
 extern "C" {
 
 // Clusters of `split` CTAs of the tile `tn` (16, 32, 64, 128) that the current device runs at once.
-int forms_clusters(int tn, int split) { return clusters(tn, split); }
+int forms_clusters(int tn, int split) {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess ? clusters(dev, tn, split) : -1;
+}
+
+// The form that a problem takes on a GPU of num_sms SMs where fit[4 i + j] clusters of 2^j CTAs of the i-th token
+// tile (16, 32, 64, 128) run at once (negative: the driver could not say): tile and split.
+void forms_pick(int64_t M, int64_t N, int64_t K, int num_sms, const int* fit, int* tn, int* split) {
+    const Form f = pick_form(M, N, (K + kGroup8 - 1) / kGroup8, num_sms, [fit](int t, int s) {
+        return fit[4 * (t == 16 ? 0 : t == 32 ? 1 : t == 64 ? 2 : 3) + (s == 1 ? 0 : s == 2 ? 1 : s == 4 ? 2 : 3)];
+    });
+    *tn = f.tn;
+    *split = f.split;
+}
 
 // One launch of a form: tn 0 (pairs of CTAs) or the token tile, on at most num_sms SMs.  copy_blocks: a
 // CTA's copies stop before this block of its own (-1: none).

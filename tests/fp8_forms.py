@@ -29,7 +29,17 @@ def lib():
     P, I, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
     so.forms_run.argtypes = [I, I, P, P, P, P, P, P, I, L, L, L, P, L, L, I, P]
     so.forms_clusters.argtypes = [I, I]
+    so.forms_pick.argtypes = [L, L, L, I, P, ctypes.POINTER(I), ctypes.POINTER(I)]
+    so.forms_pick.restype = None
     return so
+
+
+def pick(M, N, K, num_sms, fit):
+    """The (tile, split) of a problem; fit(tile, split): the clusters that run at once."""
+    table = (ctypes.c_int * 16)(*(fit(t, s) for t in TILES for s in SPLITS))
+    tn, split = ctypes.c_int(), ctypes.c_int()
+    lib().forms_pick(M, N, K, num_sms, table, ctypes.byref(tn), ctypes.byref(split))
+    return tn.value, split.value
 
 
 def fits(tn, split, M, N, K, num_sms):

@@ -12,10 +12,10 @@
 // columns (pairs of CTAs, below).  For few tokens the roles are swapped.  Operand tiles come straight
 // from the caller's row-major arrays by TMA, 128 columns = one scale block wide, 128-byte swizzled;
 // rows past M or N and columns past K read as zeros, which add nothing to the products.
+#include "device_memo.h"
 #include "fp8_ptx.cuh"
 #include "ops_internal.h"
 
-#include <atomic>
 #include <cuda_bf16.h>
 
 namespace w4a8 {
@@ -866,33 +866,32 @@ cudaError_t launch(Kernel kernel, int smem_bytes, bool* attr_done, int64_t grid,
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// How many clusters of `split` CTAs of the one-CTA kernel run at once (one CTA to an SM, clusters within
-// a GPC, so not num_sms / split: of eight CTAs fewer than 16); asked once.
+// How many clusters of `split` CTAs of the one-CTA kernel run at once on device `dev`, the current one (one
+// CTA to an SM, clusters within a GPC, so not num_sms / split: of eight CTAs fewer than 16).  Asked once a
+// device; minus a cudaError_t where the driver could not say.
+constexpr int kMaxSplit = 8;
 template <int TN>
-int tok_clusters(int split) {
+int tok_clusters(int dev, int split) {
     using T = Tok<TN>;
-    static std::atomic<int> known[9] = {};
-    int n = known[split].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(split));
-    cfg.blockDim = dim3(T::kThreads);
-    cfg.dynamicSmemBytes = T::kSmemBytes;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(fp8_tok_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, fp8_tok_kernel<TN>, &cfg) != cudaSuccess || n < 1) {
-        (void)cudaGetLastError();
-        return 1;  // not remembered
-    }
-    known[split].store(n, std::memory_order_relaxed);
-    return n;
+    static DeviceMemo<64, kMaxSplit + 1> memo;
+    return memo.get(dev, split, [split] {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(split));
+        cfg.blockDim = dim3(T::kThreads);
+        cfg.dynamicSmemBytes = T::kSmemBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        cudaError_t e = cudaFuncSetAttribute(fp8_tok_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, fp8_tok_kernel<TN>, &cfg);
+        if (e != cudaSuccess) (void)cudaGetLastError();
+        return e == cudaSuccess ? n : -static_cast<int>(e);
+    });
 }
 
 template <int TN>
@@ -932,12 +931,18 @@ double form_us(double start, double block, double end, int64_t tiles, int64_t sl
 struct Form {
     int tn, split;
 };
-int clusters(int tn, int split) {
-    return tn == 16 ? tok_clusters<16>(split) : tn == 32 ? tok_clusters<32>(split) : tn == 64 ? tok_clusters<64>(split)
-                                                                                              : tok_clusters<128>(split);
+int clusters(int dev, int tn, int split) {
+    return tn == 16   ? tok_clusters<16>(dev, split)
+           : tn == 32 ? tok_clusters<32>(dev, split)
+           : tn == 64 ? tok_clusters<64>(dev, split)
+                      : tok_clusters<128>(dev, split);
 }
 
-Form pick_form(int64_t M, int64_t N, int64_t nb, int num_sms) {
+// `fit(tn, split)`: how many of a split's clusters run at once.  Where that fails (a negative answer) no form
+// is picked but that answer returned as `split`, with tn -1: a form picked without it would sum in another
+// order than the same call's next.
+template <typename Fit>
+Form pick_form(int64_t M, int64_t N, int64_t nb, int num_sms, Fit&& fit) {
     const int64_t n128 = (N + 127) / 128;
     Form best{0, 1};
     double us = form_us(1.5, 0.418, 2.7, ((M + 255) / 256) * ((N + 255) / 256), num_sms / 2, nb);
@@ -946,10 +951,13 @@ Form pick_form(int64_t M, int64_t N, int64_t nb, int num_sms) {
     for (int i = 0; i < 4; ++i) {
         const int tn = tns[i];
         const int64_t tiles = ((M + tn - 1) / tn) * n128;
-        for (int split = 1, log = 0; split <= 8 && split <= nb; split *= 2, ++log) {
+        for (int split = 1, log = 0; split <= kMaxSplit && split <= nb; split *= 2, ++log) {
             // a split has one tile to a cluster, all of them running at once (with eight CTAs a tile and 16
             // tiles, two waves of clusters, 16 x 6144 -> 2048 took 11.4 us against 6.3 with four)
-            if (split > 1 && (tiles * split > num_sms || tiles > clusters(tn, split))) break;
+            if (split > 1 && tiles * split > num_sms) break;
+            const int most = split > 1 ? fit(tn, split) : 1;
+            if (most < 0) return Form{-1, most};
+            if (split > 1 && tiles > most) break;
             // handing the parts over: 1 x 6144 -> 1024 took 8.9, 6.7, 5.4 and 4.9 us on one, two, four and
             // eight CTAs a tile, 1 x 1024 -> 1024 3.6, 3.8, 3.7 and 4.1; with 64-token tiles 128 x 6144 ->
             // 1024 9.7 on two and 8.0 on four
@@ -989,7 +997,13 @@ cudaError_t launch_form(const Fp8Args& a, Form f, int num_sms, cudaStream_t s) {
 
 cudaError_t launch_fp8_linear(const Fp8Args& a, int num_sms, cudaStream_t s) {
     if (num_sms < 1) return cudaErrorInvalidValue;
-    return launch_form(a, pick_form(a.M, a.N, (a.K + kGroup8 - 1) / kGroup8, num_sms), num_sms, s);
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const Form f = pick_form(a.M, a.N, (a.K + kGroup8 - 1) / kGroup8, num_sms,
+                             [dev](int tn, int split) { return clusters(dev, tn, split); });
+    if (f.tn < 0) return static_cast<cudaError_t>(-f.split);
+    return launch_form(a, f, num_sms, s);
 }
 
 }  // namespace w4a8
