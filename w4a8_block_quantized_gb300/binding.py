@@ -706,7 +706,7 @@ def swiglu_quant_fp8(gate, up, a_q=None, a_scale=None, stream=None):
     try:
         M, K = shape = gate.shape
         index, dt, strides = gate.get_device(), gate.dtype, gate.stride()
-        code, ld = _IN_DTYPES[dt], strides[0]
+        code, ld = _IN_DTYPES[dt], strides[0] if M > 1 else K  # the stride of a single row says nothing
         fits = up.shape == shape and up.dtype is dt and up.get_device() == index and up.stride() == strides and \
             strides[1] == 1 and ld >= K and a_q.dtype is _E8 and a_scale.dtype is _F32 and a_q.shape == shape and \
             a_scale.shape == ((K + 127) // 128, M) and a_q.get_device() == index and \
