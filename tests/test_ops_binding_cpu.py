@@ -1,4 +1,7 @@
 """The binding's calls around the linears, without a GPU: what reaches the library."""
+import os
+import subprocess
+import sys
 import types
 
 import pytest
@@ -49,3 +52,17 @@ def test_row_stride_of_gate_and_up(calls, M, width, want):
     gate, up = OnDevice(gu[:, :256]), OnDevice(gu[:, 256:512])
     binding.swiglu_quant_fp8(gate, up, a_q=OnDevice(torch.zeros((M, 256)).to(E8)), a_scale=OnDevice(torch.zeros((2, M))))
     assert [c[2] for c in calls] == [want]
+
+
+def test_import_without_torch_private_names():
+    """A torch that lacks the private names of the short host path (one without CUDA, say): the module imports, and the
+    public calls stand in."""
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "from w4a8_block_quantized_gb300 import binding as b\n"
+            "torch.cuda.current_stream = lambda index: type('S', (), dict(cuda_stream=index + 40))\n"
+            "assert b._current_device is torch.cuda.current_device and b._raw_stream(2) == 42\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr

@@ -514,7 +514,10 @@ def linear_act(act, wq, w_scale, w_zero, M: int, N: int, K: int, bias=None, y=No
 # and the current stream is taken as a raw handle.  Measured on the GPU's host, one token through
 # rmsnorm_quant: 13.7 -> 5.8 us a call (the library call itself 2.6; a stream object alone costs 2.8,
 # the raw handle 0.08).
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# (They are not public torch names, and a torch without CUDA lacks them: the public calls stand in.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _handle(index: int, stream) -> int:
