@@ -30,7 +30,7 @@
  *     asynchronous: W4A8_OK means the work was validated and enqueued.
  *   - Shapes: K must be a positive multiple of 64; M >= 0 and N >= 0 (M == 0 or
  *     N == 0 is an empty problem: nothing is launched and W4A8_OK is returned);
- *     M, N, K <= 2^31 - 1.
+ *     M, N, K <= 2^31 - 1.  (The e4m3 calls below take a K of whole 16s.)
  *   - Alignment: x, a_q, wq, y and workspace must be 16-byte aligned; the other arrays
  *     naturally aligned for their element type.
  *   - A violated precondition returns a negative status and launches nothing.
@@ -54,9 +54,10 @@ extern "C" {
 
 typedef enum {
     W4A8_OK = 0,
-    W4A8_ERR_ARG = -1,        /* NULL pointer or negative size */
+    W4A8_ERR_ARG = -1,        /* NULL pointer, negative size, unknown type, value out of range */
     W4A8_ERR_ALIGN = -2,      /* pointer misaligned */
-    W4A8_ERR_SHAPE = -3,      /* K not a positive multiple of 64, size too large, bad window */
+    W4A8_ERR_SHAPE = -3,      /* K not a positive multiple of 64 (of 16 for the e4m3 calls), rows
+                               * closer than K, size too large, bad window */
     W4A8_ERR_CUDA = -4,       /* a CUDA runtime call or a launch failed */
     W4A8_ERR_TIMEOUT = -5,    /* a kernel gave up on a bounded wait (read by w4a8_sync_status) */
     W4A8_ERR_WORKSPACE = -6,  /* workspace NULL or smaller than the *_workspace_bytes value */
@@ -316,7 +317,8 @@ int w4a8_quant_fp8(const void *x, int in_dtype, uint8_t *a_q, float *a_scale, in
  * a_q e4m3 [M][K], a_scale fp32 [ceil(K/128)][M] (what the calls above write), w_q e4m3 [N][K],
  * w_scale fp32 [ceil(N/128)][ceil(K/128)] (one per 128 x 128 weights), bias fp32 [N] or NULL;
  * y [M][N] of out_dtype W4A8_OUT_F32 or W4A8_OUT_BF16 (anything else: W4A8_ERR_ARG).  K must be a
- * positive multiple of 16; M and N are any sizes.  Inside a block the tensor cores sum in fp32;
+ * positive multiple of 16; M and N are any sizes with
+ * ceil(M / 32) * ceil(N / 128) * ceil(K / 128) < 2^31 (W4A8_ERR_SHAPE otherwise).  Inside a block the tensor cores sum in fp32;
  * the blocks are summed in fp32 in an order that depends only on (M, N, K) and the GPU, so equal
  * calls give equal bits.  A NaN code (0x7f, 0xff) makes its outputs NaN.
  * 16-byte alignment: a_q, w_q, y; 4 bytes: a_scale, w_scale, bias. */

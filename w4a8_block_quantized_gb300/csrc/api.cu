@@ -256,9 +256,10 @@ int w4a8_abi_version(void) { return 204; }
 const char* w4a8_status_string(int status) {
     switch (status) {
         case W4A8_OK: return "ok";
-        case W4A8_ERR_ARG: return "invalid argument (null pointer or negative size)";
+        case W4A8_ERR_ARG: return "invalid argument (null pointer, negative size, or an unknown type or value out of range)";
         case W4A8_ERR_ALIGN: return "pointer misaligned";
-        case W4A8_ERR_SHAPE: return "unsupported shape (K must be a positive multiple of 64)";
+        case W4A8_ERR_SHAPE: return "unsupported shape (K must be a positive multiple of 64, of 16 for the e4m3 calls; a row stride at least K; "
+                                   "sizes are limited)";
         case W4A8_ERR_CUDA: return "CUDA error";
         case W4A8_ERR_TIMEOUT: return "a kernel gave up on a bounded wait";
         case W4A8_ERR_WORKSPACE: return "workspace missing or too small";

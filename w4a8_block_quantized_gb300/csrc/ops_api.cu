@@ -182,7 +182,8 @@ int w4a8_fp8_linear(const uint8_t* a_q, const float* a_scale, const uint8_t* w_q
                     const float* bias, void* y, int out_dtype, int64_t M, int64_t N, int64_t K, void* stream) {
     if (M < 0 || N < 0 || (out_dtype != W4A8_OUT_F32 && out_dtype != W4A8_OUT_BF16)) return W4A8_ERR_ARG;
     if (K <= 0 || K % 16 != 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return W4A8_ERR_SHAPE;
-    // the kernels count a CTA's blocks (output tiles x K/128) in 32 bits; the smallest tile is 128 x 32
+    // the kernels count tiles and a CTA's blocks (tiles x K/128) in 32 unsigned bits; the smallest tile, 128 x 16,
+    // has at most twice the number counted here
     const int64_t tiles = ((M + 31) / 32) * ((N + kGroup8 - 1) / kGroup8);
     if (tiles > kMaxDim / ((K + kGroup8 - 1) / kGroup8)) return W4A8_ERR_SHAPE;
     if (M == 0 || N == 0) return W4A8_OK;
