@@ -282,8 +282,10 @@ int w4a8_prefill_linear_host(const float *x_host, const uint8_t *wq, const uint1
  *             a_scale[b][m] = v / 448 * r; 0 and 0 where v < 2^-100: the arrays that
  *             w4a8_fp8_linear takes.  K must be a positive multiple of 16 (the last block may be
  *             short); a_q has [M][K] bytes and a_scale [ceil(K/128)][M] floats.
- * Up to the codes every step is one fp32 IEEE operation (swiglu: after t), so the codes of rmsnorm
- * and quant are defined bit for bit; sums of squares are taken in fp32, in an order that depends on K
+ * Up to the codes every step is one fp32 IEEE operation, so the codes of rmsnorm and quant are defined
+ * bit for bit; swiglu's from its t on, which takes an approximate power and reciprocal: t is within
+ * (5.1 + (4.1 + 1.23 |gate|) / (1 + exp(gate))) * 2^-24 of its magnitude (8 units of 2^-24 for gates above
+ * 0, 116 at -87), and 0 for gates below -87.3, where it is under 1.1e-36 |up|; sums of squares are taken in fp32, in an order that depends on K
  * alone: a row's codes and scales are the same in any batch.
  *   - in_dtype: the type of x, residual, residual_out, gate and up, W4A8_IN_F32 or W4A8_IN_BF16
  *     (anything else: W4A8_ERR_ARG).  gamma is fp32 [K], eps finite and > 0 (W4A8_ERR_ARG).

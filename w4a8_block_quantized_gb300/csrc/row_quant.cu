@@ -136,9 +136,12 @@ __device__ __forceinline__ void source(const RowArgs& a, int64_t m, int64_t k, c
     } else if constexpr (SRC == kSrcSwiglu) {
         const Chunk u = values(in.y);
         // g u / (1 + 2^(-g log2 e)), two values per instruction but for the power and the reciprocal, which
-        // flush subnormals: for g below -87 the power is infinite or its reciprocal 0, and the product 0,
-        // its limit to within 1e-36 u (through __expf and __fdividef, which guard those ranges, the
-        // kernel issued 25 instructions a value and took 101 us at 8192 x 14336 for 90)
+        // flush subnormals: for g below -87.3 the power is infinite or its reciprocal 0, and the product 0,
+        // its limit to within 1.1e-36 u (through __expf and __fdividef, which guard those ranges, the
+        // kernel issued 25 instructions a value and took 101 us at 8192 x 14336 for 90).  The error, in
+        // units U = 2^-24 of t and with e = 2^(-g log2 e): the constant is 0.224 U off and its product rounded,
+        // so e is 1.224 |g| off; the power's own error is at most 2^-22, 4 U; both count e / (1 + e) in the
+        // sum, which is rounded (1); the reciprocal's is at most 2^-23 (2); two products (2).
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             const uint64_t g = pk2(t.v[i], t.v[i + 1]);
