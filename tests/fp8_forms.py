@@ -49,12 +49,13 @@ def fits(tn, split, M, N, K, num_sms):
     return split == 1 or (split <= -(-K // 128) and tiles * split <= num_sms and tiles <= lib().forms_clusters(tn, split))
 
 
-def run(form, a, sa, w, sw, bias=None, y=None, out_dtype=torch.float32, limit_us=1_000_000, copy_blocks=-1, num_sms=None):
+def run(form, a, sa, w, sw, bias=None, y=None, out_dtype=torch.float32, limit_us=1_000_000, copy_blocks=-1, num_sms=None,
+        status=None):
     """(y, status word) of one launch, on the current stream."""
     (M, K), N = a.shape, w.shape[0]
     num_sms = torch.cuda.get_device_properties(0).multi_processor_count if num_sms is None else num_sms
     y = torch.empty((M, N), dtype=out_dtype, device="cuda") if y is None else y
-    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda") if status is None else status
     rc = lib().forms_run(*form, a.data_ptr(), sa.data_ptr(), w.data_ptr(), sw.data_ptr(),
                          None if bias is None else bias.data_ptr(), y.data_ptr(), int(y.dtype == torch.bfloat16), M, N, K,
                          status.data_ptr(), limit_us, copy_blocks, num_sms, torch.cuda.current_stream().cuda_stream)
