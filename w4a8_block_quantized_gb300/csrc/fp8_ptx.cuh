@@ -80,11 +80,6 @@ __device__ __forceinline__ void cp_async_wait() {
 
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// This thread's arrival on a named barrier that others wait on (named_bar_sync).
-__device__ __forceinline__ void named_bar_arrive(int id, int threads) {
-    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // The forms for a pair of CTAs (ranks 0 and 1 of a two-CTA cluster), whose barriers sit at the same
 // offset in both and whose MMAs the even CTA issues.
 

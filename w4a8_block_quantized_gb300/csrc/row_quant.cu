@@ -390,20 +390,20 @@ __global__ void __launch_bounds__(512) row_quant_kernel(const RowArgs a, int W, 
         [&](int i) { return load_gamma<SRC>(a, 8 * (c0 + i * by)); }, [] {});
 }
 
-// Many rows: the rows come through shared memory, copied by the async engine `stages` rows ahead of each
-// group of W warps, so that the bytes in flight neither cost registers nor stop while a row is worked
+// Many bf16 rows of a norm: they come through shared memory, copied by the async engine `stages` rows ahead
+// of each group of W warps, so that the bytes in flight neither cost registers nor stop while a row is worked
 // on.  A group walks rows m, m + groups, ...; its first thread refills a stage once the group has read
-// it.  gamma stays in registers.  Shared memory: [group][stage][x | y][K], then a barrier per stage.
-template <int SRC, int FORM, bool BF16, int C>
+// it.  gamma stays in registers.  Shared memory: [group][stage][x | residual][K], then a barrier per stage.
+template <int FORM>
 __global__ void __launch_bounds__(512) row_stream_kernel(const RowArgs a, int W, int stages) {
     griddep_launch_dependents();
     extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int C = 4, kEl = 2;
     __shared__ float slots[2][16 * (1 + C)];
     __shared__ uint32_t abort_flag;
-    constexpr int kEl = BF16 ? 2 : 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rsub = warp / W, wg = warp - rsub * W, rpc = static_cast<int>(blockDim.x >> 5) / W;
-    const bool two = SRC == kSrcSwiglu || (SRC == kSrcNorm && a.residual);
+    const bool two = a.residual != nullptr;
     const uint32_t bytes = static_cast<uint32_t>(a.K) * kEl, stage_bytes = bytes * (two ? 2 : 1);
     uint8_t* ring = smem + static_cast<uint32_t>(rsub * stages) * stage_bytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<uint32_t>(rpc * stages) * stage_bytes) + rsub * stages;
@@ -422,10 +422,7 @@ __global__ void __launch_bounds__(512) row_stream_kernel(const RowArgs a, int W,
         mbar_arrive_expect_tx(full + s, stage_bytes);
         bulk_load(ring + s * stage_bytes, static_cast<const uint8_t*>(a.x) + m * a.ld * kEl, bytes, full + s);
         if (two)
-            bulk_load(ring + s * stage_bytes + bytes,
-                      SRC == kSrcNorm ? static_cast<const uint8_t*>(a.residual) + m * a.K * kEl
-                                      : static_cast<const uint8_t*>(a.up) + m * a.ld * kEl,
-                      bytes, full + s);
+            bulk_load(ring + s * stage_bytes + bytes, static_cast<const uint8_t*>(a.residual) + m * a.K * kEl, bytes, full + s);
     };
     if (leader)
         for (int s = 0; s < stages && first + s * step < a.M; ++s) fill(first + s * step, s);
@@ -433,7 +430,7 @@ __global__ void __launch_bounds__(512) row_stream_kernel(const RowArgs a, int W,
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int64_t c = static_cast<int64_t>(i * W + wg) * 32 + lane;
-        if (c < n8) gamma[i] = load_gamma<SRC>(a, 8 * c);
+        if (c < n8) gamma[i] = load_gamma<kSrcNorm>(a, 8 * c);
     }
     // after a wait gave up the rest of the rows is worked on as it is (the status word says so); the
     // stages in flight are left to land below
@@ -444,27 +441,19 @@ __global__ void __launch_bounds__(512) row_stream_kernel(const RowArgs a, int W,
         if (ok) ok = mbar_wait(full + s, phase, ctl);
         __syncwarp();
         const uint8_t* st = ring + s * stage_bytes;
-        work_row<SRC, FORM, BF16, C>(
+        work_row<kSrcNorm, FORM, true, C>(
             a, m, true, 0, W, wg, lane, slots[par] + rsub * W * (1 + C), 1 + rsub,
             [&](int i) {
                 const uint32_t at = static_cast<uint32_t>((i * W + wg) * 32 + lane) * 8 * kEl;
-                Inputs<SRC, BF16> in;
-#pragma unroll
-                for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
-                    in.x.w[h] = *reinterpret_cast<const uint4*>(st + at + 16 * h);
-                    if (two) in.y.w[h] = *reinterpret_cast<const uint4*>(st + bytes + at + 16 * h);
-                }
+                Inputs<kSrcNorm, true> in;
+                in.x.w[0] = *reinterpret_cast<const uint4*>(st + at);
+                if (two) in.y.w[0] = *reinterpret_cast<const uint4*>(st + bytes + at);
                 return in;
             },
             [&](int i) { return gamma[i]; },
             [&] {
-                if (SRC != kSrcNorm && FORM == kFormE4m3) {  // the forms without a reduction
-                    if (W > 1) named_bar_sync(1 + rsub, W * 32);
-                    else __syncwarp();
-                } else if (W == 1) {
-                    __syncwarp();
-                }
-                // every warp of the row has read the stage: its next row may land
+                // every warp of the row has read the stage (they met in the reduction): its next row may land
+                if (W == 1) __syncwarp();
                 if (leader && ok && m + stages * step < a.M) fill(m + stages * step, s);
             });
         if (++s == stages) s = 0, phase ^= 1u;
@@ -537,7 +526,8 @@ cudaError_t launch_pdl(void (*kernel)(Args...), int64_t grid, int threads, size_
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Blocks per SM of the streaming kernel and rows in flight a group.  Measured on 16384 x 4096 bf16 (us):
+// Blocks launched per SM of the streaming kernel (two are resident, by registers), and rows in flight a
+// group.  Measured on 16384 x 4096 bf16 (us):
 // two stages and 4 / 6 / 8 blocks 73.3 / 74.3 / 72.9, three stages (smaller blocks) 78.3, one 87.1; on
 // 4096 x 14336 4 / 6 / 8 blocks 70.7 / 76.1 / 76.8.
 constexpr int kStreamBlocks = 4, kStreamStages = 2;
@@ -549,8 +539,8 @@ cudaError_t run_stream(const RowArgs& a, int W, int rpc, int num_sms, cudaStream
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 64 && !attr_done[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(row_stream_kernel<kSrcNorm, FORM, true, 4>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMost + 256);
+        const cudaError_t e =
+            cudaFuncSetAttribute(row_stream_kernel<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost + 256);
         if (e != cudaSuccess) return e;
         attr_done[dev] = true;
     }
@@ -558,16 +548,17 @@ cudaError_t run_stream(const RowArgs& a, int W, int rpc, int num_sms, cudaStream
     const size_t smem = static_cast<size_t>(rpc * kStreamStages) * (stage + 8);
     const int64_t need = (a.M + rpc - 1) / rpc, cap = static_cast<int64_t>(num_sms) * kStreamBlocks;
     const int64_t rounds = (need + cap - 1) / cap;
-    return launch_pdl(row_stream_kernel<kSrcNorm, FORM, true, 4>, (need + rounds - 1) / rounds, rpc * W * 32, smem, s, a, W,
-                      kStreamStages);
+    return launch_pdl(row_stream_kernel<FORM>, (need + rounds - 1) / rounds, rpc * W * 32, smem, s, a, W, kStreamStages);
 }
 
 template <int SRC, int FORM, bool BF16>
 cudaError_t run(const RowArgs& a, int num_sms, cudaStream_t s) {
     const int64_t n8 = a.K / 8;
-    if (!kParts<SRC, FORM> && n8 > 16 * 32 * 4) {
-        row_quant_long_kernel<SRC, FORM, BF16><<<static_cast<unsigned>(a.M), 1024, 0, s>>>(a);
-        return cudaGetLastError();
+    if constexpr (!kParts<SRC, FORM>) {
+        if (n8 > 16 * 32 * 4) {
+            row_quant_long_kernel<SRC, FORM, BF16><<<static_cast<unsigned>(a.M), 1024, 0, s>>>(a);
+            return cudaGetLastError();
+        }
     }
     auto warps = [&](int C) { return static_cast<int>((n8 + 32 * C - 1) / (32 * C)); };
     // Chunks a lane.  One where its warps still fit the GPU at once (512 x 2048 bf16 to INT8: 3.5 us

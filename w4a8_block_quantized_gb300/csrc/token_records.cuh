@@ -11,8 +11,8 @@
 
 namespace w4a8 {
 
-// Two e4m3 codes in one 16-bit word, v0 in the low byte.  The inputs are small exact
-// integers (|v| <= 128 with at most 4 significant bits), so the conversion is exact.
+// Two e4m3 codes in one 16-bit word, v0 in the low byte: rounded to nearest even, 448 past the largest.  Of
+// the planes' values (integers of at most 4 significant bits up to 128) the conversion is exact.
 __device__ __forceinline__ uint32_t e4m3x2(float v0, float v1) {
     unsigned short d;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(v1), "f"(v0));
