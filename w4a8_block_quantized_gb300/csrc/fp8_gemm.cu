@@ -922,6 +922,11 @@ cudaError_t run_pair(Fp8Params& p, const Fp8Args& a, int num_sms, cudaStream_t s
 // 128-token tiles: 512 x 2048 -> 2048 11.0, 12.8, 8.5, 7.0, 10.2; 512 x 8192 -> 2048 31.2, 40.4, 22.8,
 // 16.8, 26.2; 256 x 2048 -> 2048 10.9, 7.7, 5.3, 6.8, 10.0; 512 x 2048 -> 6144 12.3, 31.3, 21.0, 16.0,
 // 17.5; 4096 x 1024 -> 2048 13.7, 45.2, 30.2, 21.5, 20.5; 8 x 4096 -> 14336 22.3, 12.3, 12.7, 17.4, 25.2.
+// Outputs of another type or width, pairs against 128-token tiles: rows of y that no 16-byte store fits cost
+// pairs 3.4 us a tile (512 x 2048 -> 6143 15.9 and 18.1, 4096 x 1024 -> 2047 20.9 and 21.5, but 2048 x 512 ->
+// 14335 46.3 and 43.2, against 22.8 and 40.9 at 14336), which counts for any N that is no multiple of 8, so
+// that the order of the sums does not depend on y's type; fp32 rows cost them 1.2 (512 x 2048 -> 6144 13.8 and
+// 18.2, 2048 x 512 -> 14336 29.7 and 42.3), which changed no choice and is not counted.
 double form_us(double start, double block, double end, int64_t tiles, int64_t slots, int64_t blocks) {
     const int64_t waves = (tiles + slots - 1) / slots;
     return start + static_cast<double>(waves) * (block * static_cast<double>(blocks) + end);
@@ -945,7 +950,7 @@ template <typename Fit>
 Form pick_form(int64_t M, int64_t N, int64_t nb, int num_sms, Fit&& fit) {
     const int64_t n128 = (N + 127) / 128;
     Form best{0, 1};
-    double us = form_us(1.5, 0.418, 2.7, ((M + 255) / 256) * ((N + 255) / 256), num_sms / 2, nb);
+    double us = form_us(1.5, 0.418, N % 8 == 0 ? 2.7 : 6.1, ((M + 255) / 256) * ((N + 255) / 256), num_sms / 2, nb);
     const int tns[4] = {16, 32, 64, 128};
     const double start[4] = {2.35, 1.9, 2.1, 2.4}, block[4] = {0.153, 0.16, 0.205, 0.335}, end[4] = {0.2, 0.75, 1.33, 2.2};
     for (int i = 0; i < 4; ++i) {
