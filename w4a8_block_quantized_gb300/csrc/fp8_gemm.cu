@@ -728,7 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             }
             it ^= 1;
 #pragma unroll 1
-            for (int b0 = 0; b0 < p.nb && all_ok(!*abort_flag); b0 += kChunk) {
+            for (int b0 = 0; b0 < p.nb; b0 += kChunk) {
                 if (b0 > 0) (void)mbar_poll(&sfull[js & 1u], (js >> 1) & 1, ctl);
                 const float* sa = scales + (js & 1u) * kScaleFloats + q * 32 + lane;
                 const float* sw = scales + (js & 1u) * kScaleFloats + kChunk * 128 + r;

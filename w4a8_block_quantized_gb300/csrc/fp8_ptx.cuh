@@ -19,16 +19,17 @@ __device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity
         : "memory");
     return ok != 0;
 }
-// mbar_wait for waits of a few hundred cycles on a kernel's critical path: up to 64 tries before the
-// abort flag and the clock are looked at.
+// mbar_wait for waits of a few hundred cycles on a kernel's critical path, after a first try: up to 64 tries
+// between looks at the abort flag and the clock.  Once the flag is up a wait costs a try and a look, so that
+// a loop of them ends soon too.
 __device__ __forceinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, const WaitCtl& ctl) {
     uint64_t t0 = 0;
 #pragma unroll 1
     for (;;) {
+        if (*ctl.abort) return false;
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
             if (mbar_try_wait_long(bar, parity)) return true;
-        if (*ctl.abort) return false;
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) t0 = now;
         if (now - t0 > ctl.limit_ns) {
