@@ -449,8 +449,9 @@ __global__ void __launch_bounds__(Tok<TN>::kThreads, 1) fp8_tok_kernel(const __g
 //   warps 4-19  drain, 4 lane quarters x 4 runs of 64 columns: a thread holds 64 sums
 //
 // Measured at 8192 x 4096 -> 14336 (bf16 out) on several GPUs: 333 to 347 us, 2.8 PFLOP/s, in short runs;
-// 368 to 386 us, 2.5 PFLOP/s, in long ones, where the power limit holds the clock at 1.7 to 1.8 GHz.  What bounds it is not the tensor
-// pipe (206 us for the MMAs alone, 258 with the copies and the issue) but what surrounds each block:
+// 368 to 386 us, 2.5 PFLOP/s, in long ones, where the power limit holds the clock at 1.7 to 1.8 GHz.  What
+// bounds it is not the tensor pipe (206 us for the MMAs alone, 258 with the copies and the issue) but what
+// surrounds each block:
 // 32768 fmas a CTA and block (256 cycles of the fp32 pipes, against 512 of the tensor pipe), and the
 // accumulators' way from a commit over the drain back to the issuer, during which their TMEM lies
 // idle (323 us without the fmas).  So:
