@@ -363,6 +363,9 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) few_kernel(const __
         if (warp == 0) *abort_flag = 0;
     }
     if (threadIdx.x < 2) tma_prefetch_map(threadIdx.x ? &p.vmap : &p.kmap);
+    // A warp's copies complete barriers that its first lane set up, and every wait reads the flag; a cluster's CTA of up to 16
+    // rows comes to no other barrier before them.
+    __syncthreads();
     griddep_wait();
     griddep_launch_dependents();  // the join's blocks may come in, and wait for this grid
     const Share share = find_share<D>(p, scan);
