@@ -25,3 +25,74 @@ def test_clusters_after_full_shared_memory(D, n, G):
     for _ in range(100):
         attend(wide)
         assert torch.equal(attend(p), first)
+
+
+def over_freed_blocks(call, *sizes):
+    """`call` on another stream while the current one still reads blocks of these many bytes that it has freed: what was
+    read of them."""
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = [torch.full((n,), 0x3C, dtype=torch.uint8, device="cuda") for n in sizes]
+    seen = [torch.empty_like(t) for t in held]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    for s, t in zip(seen, held):
+        s.copy_(t)
+    del held, t
+    got = call(side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    return got, all(bool((s == 0x3C).all()) for s in seen)
+
+
+def test_another_streams_outputs_leave_memory_in_use_alone():
+    """A call on another stream allocates its outputs and workspaces where that stream may write at once, not in blocks
+    that the current stream has just freed and still reads."""
+    cache = B().KVCache.empty(64, 8, 64, 128)
+    x, slots = normal(2, 1024, 8, 128).to(BF), torch.arange(1024, device="cuda")
+    pos, table = slots.int(), B().rope_table(128)
+    size = x.numel() * 2
+    want = B().kv_write(cache, x, x, slots, pos, table, q=x)
+    back = B().kv_read(cache, slots)
+    p = problem(5, [(300, 700)] * 2, 2, 4, 128, 32, I8)
+    need = B().attention_workspace_bytes(p["q"], p["cache"], 2, p["max_q"], p["max_kv"])
+    out = attend(p)
+    for call, expect, sizes in ((lambda s: B().rope(x, pos, table, stream=s), want, (size,)),
+                                (lambda s: B().kv_write(cache, x, x, slots, pos, table, q=x, stream=s), want, (size,)),
+                                (lambda s: torch.stack(B().kv_read(cache, slots, stream=s)), torch.stack(back), (size, size)),
+                                (lambda s: attend(p, stream=s), out, (out.numel() * 2, need))):
+        got, kept = over_freed_blocks(call, *sizes)
+        assert kept and torch.equal(got, expect)
+
+
+def test_another_streams_outputs_of_the_linears():
+    """The same of the calls around the attention."""
+    x, w = normal(1, 512, 1024), torch.ones(1024, device="cuda")
+    codes = torch.randint(0, 256, (640, 512), dtype=torch.uint8, device="cuda")
+    ws, wz = torch.full((640, 16), 0.01, dtype=torch.float16, device="cuda"), torch.full((640, 16), 8.0, dtype=torch.float16, device="cuda")
+    a, s, r = B().quant_pack(x)
+    act, pw = B().prepare_activations(x), B().prepare_weights(codes, ws, wz)
+    e, es = B().quant_fp8(x)
+    we, wes = normal(2, 640, 1024).to(E8), torch.ones((5, 8), device="cuda")
+    y, M, N, K = 512 * 640 * 4, 512, 640, 1024
+    for name, call, sizes in (
+            ("quant_pack", lambda st: B().quant_pack(x, stream=st), (M * K, M * 4, M * K // 16)),
+            ("linear", lambda st: B().linear(a, s, r, codes, ws, wz, stream=st), (y, B().linear_workspace_bytes(M, N, K))),
+            ("prefill_linear", lambda st: B().prefill_linear(x, codes, ws, wz, stream=st), (y, B().prefill_workspace_bytes(M, N, K))),
+            ("batch", lambda st: B().prefill_linear_batch([dict(x=x, wq=codes, s_w=ws, z_w=wz)], stream=st), (y, B().prefill_workspace_bytes(M, N, K))),
+            ("prefill_linear_ex", lambda st: B().prefill_linear_ex(x, codes, ws, wz, out_dtype=BF, stream=st), (y // 2, B().prefill_workspace_bytes(M, N, K))),
+            ("prepare_activations", lambda st: B().prepare_activations(x, stream=st), (B().prepared_activations_bytes(M, K),)),
+            ("prepare_weights", lambda st: B().prepare_weights(codes, ws, wz, stream=st), (B().prepared_weights_bytes(N, K),)),
+            ("linear_prepared", lambda st: B().linear_prepared(act, pw, M, N, K, stream=st), (y,)),
+            ("linear_act", lambda st: B().linear_act(act, codes, ws, wz, M, N, K, stream=st), (y,)),
+            ("rmsnorm_quant_fp8", lambda st: B().rmsnorm_quant_fp8(x, w, 1e-5, residual=x, stream=st), (M * K, M * 32, M * K * 4)),
+            ("rmsnorm_prepare", lambda st: B().rmsnorm_prepare(x, w, 1e-5, stream=st), (B().prepared_activations_bytes(M, K),)),
+            ("swiglu_quant", lambda st: B().swiglu_quant(x, x, stream=st), (M * K, M * 4, M * K // 16)),
+            ("quant_fp8", lambda st: B().quant_fp8(x, stream=st), (M * K, M * 32)),
+            ("fp8_linear", lambda st: B().fp8_linear(e, es, we, wes, stream=st), (y,))):
+        want = call(None)
+        got, kept = over_freed_blocks(call, *sizes)
+        assert kept, name
+        for g, t in zip(*((v,) if isinstance(v, torch.Tensor) else v for v in (got, want))):
+            assert (g is None and t is None) or torch.equal(g.view(torch.uint8), t.view(torch.uint8)), name

@@ -6,6 +6,7 @@ fallback: if the library is missing or the GPU is not an sm_103 part, calls rais
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -172,19 +173,42 @@ def _weights(wq, w_scale, w_zero, N: int, K: int, device):
     _arg(w_zero, torch.float16, (N, K // 64), "w_zero", device)
 
 
+def _on(stream, device):
+    """A context in which tensors are allocated for work on `stream` (None: the current one).  The caching allocator
+    hands out a block freed on a stream at once, because what that stream does next comes behind the work that still
+    uses it; another stream's work does not, so that its tensors come from memory of its own."""
+    return contextlib.nullcontext() if stream is None or stream == torch.cuda.current_stream(device) else torch.cuda.stream(stream)
+
+
+def _new(shape, dtype, device, stream):
+    """An output allocated here, for a call on `stream`.  The caller's stream is recorded too: a block that is dropped while
+    work queued there uses it goes to no other work before that is done."""
+    with _on(stream, device):
+        t = torch.empty(tuple(shape), dtype=dtype, device=device)
+    return _returned(t, stream)
+
+
+def _returned(t, stream):
+    if stream is not None and stream != torch.cuda.current_stream(t.device):
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _ws(ws, need: int, device, stream=None):
     """The caller's workspace (any dtype: its size in bytes is what the library is told), or
-    a temporary one.  A temporary is dropped when the call returns, while the library's work
-    on it is still queued on `stream`; the caching allocator is told about that stream
-    (record_stream), so it does not hand the block to other work before that work is done
-    (it otherwise tracks only the current stream, on which the block was allocated)."""
+    a temporary one, allocated for `stream` and dropped when the call returns."""
     if ws is None:
-        t = workspace(need, device)
-        if stream is not None:
-            t.record_stream(stream)
-        return t
+        with _on(stream, device):
+            return workspace(need, device)
     _arg(ws, None, None, "ws", device)
     return ws
+
+
+def _buffer(buf, need: int, device, stream, name: str):
+    """An opaque buffer that the call returns: the caller's, or one allocated for `stream`."""
+    buf = _returned(_ws(None, need, device, stream), stream) if buf is None else buf
+    _arg(buf, None, None, name, device)
+    return buf
 
 
 def linear_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -215,12 +239,7 @@ def quant_pack(x: torch.Tensor, a_q=None, a_scale=None, rowsum=None, stream=None
     _want(x, torch.float32, "x")
     M, K = x.shape
     dev = x.device
-    a_q = torch.empty((M, K), dtype=torch.int8, device=dev) if a_q is None else a_q
-    a_scale = torch.empty((M,), dtype=torch.float32, device=dev) if a_scale is None else a_scale
-    rowsum = torch.empty((M, K // 64), dtype=torch.int32, device=dev) if rowsum is None else rowsum
-    _arg(a_q, torch.int8, (M, K), "a_q", dev)
-    _arg(a_scale, torch.float32, (M,), "a_scale", dev)
-    _arg(rowsum, torch.int32, (M, K // 64), "rowsum", dev)
+    a_q, a_scale, rowsum = _int8_out(M, K, dev, a_q, a_scale, rowsum, stream)
     rc = load().w4a8_quant_pack(_ptr(x), M, K, _ptr(a_q), _ptr(a_scale), _ptr(rowsum), _stream(stream))
     _check(rc, "w4a8_quant_pack")
     return a_q, a_scale, rowsum
@@ -242,7 +261,7 @@ def linear(a_q, a_scale, rowsum, wq, w_scale, w_zero, bias=None, y=None, ws=None
     N = _rows(wq)
     _weights(wq, w_scale, w_zero, N, K, dev)
     _arg(bias, torch.float32, (N,), "bias", dev)
-    y = torch.empty((M, N), dtype=torch.float32, device=dev) if y is None else y
+    y = _new((M, N), torch.float32, dev, stream) if y is None else y
     _arg(y, torch.float32, (M, N), "y", dev)
     ws = _ws(ws, linear_workspace_bytes(M, N, K), dev, stream)
     rc = load().w4a8_linear(_ptr(a_q), _ptr(a_scale), _ptr(rowsum), _ptr(wq), _ptr(w_scale), _ptr(w_zero),
@@ -273,7 +292,7 @@ def _prefill_args(x, wq, w_scale, w_zero, bias):
 def prefill_linear(x, wq, w_scale, w_zero, bias=None, y=None, ws=None, stream=None):
     """w4a8_prefill_linear: fp32 x [M,K] -> y fp32 [M,N] (pre-pass + linear)."""
     M, N, K = _prefill_args(x, wq, w_scale, w_zero, bias)
-    y = torch.empty((M, N), dtype=torch.float32, device=x.device) if y is None else y
+    y = _new((M, N), torch.float32, x.device, stream) if y is None else y
     _arg(y, torch.float32, (M, N), "y", x.device)
     ws = _ws(ws, prefill_workspace_bytes(M, N, K), x.device, stream)
     rc = load().w4a8_prefill_linear(_ptr(x), _ptr(wq), _ptr(w_scale), _ptr(w_zero), _ptr(bias), _ptr(y),
@@ -292,13 +311,14 @@ class Batch:
     """The entries of a w4a8_prefill_linear_batch call, checked and marshalled once: a sequence
     of dicts with x, wq, s_w, z_w, optional bias, y and ws (y and ws allocated when absent),
     one M for all.  `run(stream)` makes the call; `ys` are the outputs.  The tensors are held
-    for the life of the object."""
+    for the life of the object.  What is allocated here is allocated for `stream` (None: the current one); a
+    run on another stream comes behind the work that was queued there by then."""
 
     def __init__(self, entries, stream=None):
         entries = list(entries)
         self.count = len(entries)
         self.refs = (LinearRef * max(1, self.count))()
-        self.keep, self.ys = [], []
+        self.keep, self.ys, self.own, self.stream = [], [], [], stream
         self.M = 0
         for i, e in enumerate(entries):
             x, wq, sw, zw, bias = e["x"], e["wq"], e["s_w"], e["z_w"], e.get("bias")
@@ -308,7 +328,7 @@ class Batch:
             elif m != self.M:
                 raise ValueError(f"entry {i}: x has {m} rows, the batch {self.M}")
             y = e.get("y")
-            y = torch.empty((m, N), dtype=torch.float32, device=x.device) if y is None else y
+            y = _new((m, N), torch.float32, x.device, stream) if y is None else y
             _arg(y, torch.float32, (m, N), "y", x.device)
             ws = _ws(e.get("ws"), prefill_workspace_bytes(m, N, K), x.device, stream)
             self.refs[i] = LinearRef(x.data_ptr(), wq.data_ptr(), sw.data_ptr(), zw.data_ptr(),
@@ -316,8 +336,16 @@ class Batch:
                                      _nbytes(ws))
             self.keep += [x, wq, sw, zw, bias, ws]
             self.ys.append(y)
+            self.own += [t for t, given in ((y, e.get("y")), (ws, e.get("ws"))) if given is None]
+        if stream is None and self.own:
+            self.stream = torch.cuda.current_stream(self.own[0].device)
 
     def run(self, stream=None):
+        if self.own:
+            used = torch.cuda.current_stream(self.own[0].device) if stream is None else stream
+            if used != self.stream:
+                for t in self.own:
+                    t.record_stream(used)
         rc = load().w4a8_prefill_linear_batch(ctypes.cast(self.refs, _P), self.count, self.M, _stream(stream))
         _check(rc, "w4a8_prefill_linear_batch")
         return self.ys
@@ -333,7 +361,7 @@ def prefill_linear_noalloc(x, wq, w_scale, w_zero, bias=None, y=None, stream=Non
     """w4a8_prefill_linear_noalloc: the fused call on the library's static scratch buffer,
     for callers that cannot allocate device memory.  Serialize calls that could overlap."""
     M, N, K = _prefill_args(x, wq, w_scale, w_zero, bias)
-    y = torch.empty((M, N), dtype=torch.float32, device=x.device) if y is None else y
+    y = _new((M, N), torch.float32, x.device, stream) if y is None else y
     _arg(y, torch.float32, (M, N), "y", x.device)
     rc = load().w4a8_prefill_linear_noalloc(_ptr(x), _ptr(wq), _ptr(w_scale), _ptr(w_zero), _ptr(bias), _ptr(y),
                                             M, N, K, _stream(stream))
@@ -395,8 +423,7 @@ def prepare_activations(x, act=None, stream=None):
     """w4a8_prepare_activations: the pre-pass into an opaque buffer (returned)."""
     _want(x, torch.float32, "x")
     M, K = x.shape
-    act = workspace(prepared_activations_bytes(M, K), x.device) if act is None else act
-    _arg(act, None, None, "act", x.device)
+    act = _buffer(act, prepared_activations_bytes(M, K), x.device, stream, "act")
     rc = load().w4a8_prepare_activations(_ptr(x), M, K, _ptr(act), _nbytes(act), _stream(stream))
     _check(rc, "w4a8_prepare_activations")
     return act
@@ -408,19 +435,18 @@ def prepare_weights(wq, w_scale, w_zero, pw=None, stream=None):
     N = _rows(wq)
     K = 2 * wq.shape[1]
     _weights(wq, w_scale, w_zero, N, K, wq.device)
-    pw = workspace(prepared_weights_bytes(N, K), wq.device) if pw is None else pw
-    _arg(pw, None, None, "pw", wq.device)
+    pw = _buffer(pw, prepared_weights_bytes(N, K), wq.device, stream, "pw")
     rc = load().w4a8_prepare_weights(_ptr(wq), _ptr(w_scale), _ptr(w_zero), N, K, _ptr(pw), _nbytes(pw),
                                      _stream(stream))
     _check(rc, "w4a8_prepare_weights")
     return pw
 
 
-def _out(y, shape, device, out_dtype):
+def _out(y, shape, device, out_dtype, stream):
     dt = torch.float32 if out_dtype is None else out_dtype
     if dt not in _OUT_DTYPES:
         raise TypeError(f"y: unsupported output dtype {dt}")
-    y = torch.empty(shape, dtype=dt, device=device) if y is None else y
+    y = _new(shape, dt, device, stream) if y is None else y
     _arg(y, dt, shape, "y", device)
     return y, _OUT_DTYPES[dt]
 
@@ -429,7 +455,7 @@ def prefill_linear_ex(x, wq, w_scale, w_zero, bias=None, y=None, out_dtype=None,
                       ws=None, stream=None):
     """w4a8_prefill_linear_ex: the fused call with the epilogue clamp and an fp32 or bf16 y."""
     M, N, K = _prefill_args(x, wq, w_scale, w_zero, bias)
-    y, code = _out(y, (M, N), x.device, out_dtype if y is None else y.dtype)
+    y, code = _out(y, (M, N), x.device, out_dtype if y is None else y.dtype, stream)
     ws = _ws(ws, prefill_workspace_bytes(M, N, K), x.device, stream)
     rc = load().w4a8_prefill_linear_ex(_ptr(x), _ptr(wq), _ptr(w_scale), _ptr(w_zero), _ptr(bias), _ptr(y), code,
                                        float(clamp[0]), float(clamp[1]), M, N, K, _ptr(ws), _nbytes(ws),
@@ -446,7 +472,7 @@ def linear_ex(a_q, a_scale, rowsum, wq, w_scale, w_zero, bias=None, y=None, out_
     N = _rows(wq)
     _weights(wq, w_scale, w_zero, N, K, dev)
     _arg(bias, torch.float32, (N,), "bias", dev)
-    y, code = _out(y, (M, N), dev, out_dtype if y is None else y.dtype)
+    y, code = _out(y, (M, N), dev, out_dtype if y is None else y.dtype, stream)
     ws = _ws(ws, linear_workspace_bytes(M, N, K), dev, stream)
     rc = load().w4a8_linear_ex(_ptr(a_q), _ptr(a_scale), _ptr(rowsum), _ptr(wq), _ptr(w_scale), _ptr(w_zero),
                                _ptr(bias), _ptr(y), code, float(clamp[0]), float(clamp[1]), M, N, K, _ptr(ws),
@@ -475,7 +501,7 @@ def linear_prepared_ex(act, pw, M: int, N: int, K: int, bias=None, y=None, out_d
                        clamp=(-math.inf, math.inf), stream=None):
     """w4a8_linear_prepared_ex: prepared operands, epilogue clamp, fp32 or bf16 y."""
     dev = _prepared(act, pw, bias, M, N, K)
-    y, code = _out(y, (M, N), dev, out_dtype if y is None else y.dtype)
+    y, code = _out(y, (M, N), dev, out_dtype if y is None else y.dtype, stream)
     rc = load().w4a8_linear_prepared_ex(_ptr(act), _ptr(pw), _ptr(bias), _ptr(y), code, float(clamp[0]),
                                         float(clamp[1]), M, N, K, _stream(stream))
     _check(rc, "w4a8_linear_prepared_ex")
@@ -485,7 +511,7 @@ def linear_prepared_ex(act, pw, M: int, N: int, K: int, bias=None, y=None, out_d
 def linear_prepared(act, pw, M: int, N: int, K: int, bias=None, y=None, stream=None):
     """w4a8_linear_prepared: contraction + epilogue from prepared operands -> y fp32 [M,N]."""
     dev = _prepared(act, pw, bias, M, N, K)
-    y = torch.empty((M, N), dtype=torch.float32, device=dev) if y is None else y
+    y = _new((M, N), torch.float32, dev, stream) if y is None else y
     _arg(y, torch.float32, (M, N), "y", dev)
     rc = load().w4a8_linear_prepared(_ptr(act), _ptr(pw), _ptr(bias), _ptr(y), M, N, K, _stream(stream))
     _check(rc, "w4a8_linear_prepared")
@@ -507,7 +533,7 @@ def linear_act(act, wq, w_scale, w_zero, M: int, N: int, K: int, bias=None, y=No
         _arg(act, None, None, "act", dev, min_bytes=prepared_activations_bytes(M, K))
     _weights(wq, w_scale, w_zero, N, K, dev)
     _arg(bias, torch.float32, (N,), "bias", dev)
-    y = torch.empty((M, N), dtype=torch.float32, device=dev) if y is None else y
+    y = _new((M, N), torch.float32, dev, stream) if y is None else y
     _arg(y, torch.float32, (M, N), "y", dev)
     ws = _ws(ws, linear_act_workspace_bytes(M, N, K), dev, stream)
     rc = load().w4a8_linear_act(_ptr(act), _ptr(wq), _ptr(w_scale), _ptr(w_zero), _ptr(bias), _ptr(y), M, N, K,
@@ -548,7 +574,7 @@ def _rows_in(x, name: str):
     return x.shape[0], x.shape[1], _IN_DTYPES[x.dtype], x.device
 
 
-def _norm_in(x, weight, residual, residual_out):
+def _norm_in(x, weight, residual, residual_out, stream):
     M, K, code, dev = _rows_in(x, "x")
     _arg(weight, torch.float32, (K,), "weight", dev)
     if weight is None:
@@ -558,7 +584,7 @@ def _norm_in(x, weight, residual, residual_out):
         if residual_out is not None:
             raise ValueError("residual_out without a residual")
     elif residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = _new((M, K), x.dtype, dev, stream)
     else:
         _arg(residual_out, x.dtype, (M, K), "residual_out", dev)
     return M, K, code, dev, residual_out
@@ -592,20 +618,20 @@ def _gate_up(gate, up):
     return M, K, (ld if M > 1 else K), _IN_DTYPES[gate.dtype], gate.device
 
 
-def _int8_out(M, K, dev, a_q, a_scale, rowsum):
-    a_q = torch.empty((M, K), dtype=_I8, device=dev) if a_q is None else a_q
-    a_scale = torch.empty((M,), dtype=_F32, device=dev) if a_scale is None else a_scale
-    rowsum = torch.empty((M, K // 64), dtype=_I32, device=dev) if rowsum is None else rowsum
+def _int8_out(M, K, dev, a_q, a_scale, rowsum, stream):
+    a_q = _new((M, K), _I8, dev, stream) if a_q is None else a_q
+    a_scale = _new((M,), _F32, dev, stream) if a_scale is None else a_scale
+    rowsum = _new((M, K // 64), _I32, dev, stream) if rowsum is None else rowsum
     _arg(a_q, _I8, (M, K), "a_q", dev)
     _arg(a_scale, _F32, (M,), "a_scale", dev)
     _arg(rowsum, _I32, (M, K // 64), "rowsum", dev)
     return a_q, a_scale, rowsum
 
 
-def _e4m3_out(M, K, dev, a_q, a_scale):
+def _e4m3_out(M, K, dev, a_q, a_scale, stream):
     nb = (K + 127) // 128
-    a_q = torch.empty((M, K), dtype=_E8, device=dev) if a_q is None else a_q
-    a_scale = torch.empty((nb, M), dtype=_F32, device=dev) if a_scale is None else a_scale
+    a_q = _new((M, K), _E8, dev, stream) if a_q is None else a_q
+    a_scale = _new((nb, M), _F32, dev, stream) if a_scale is None else a_scale
     _arg(a_q, _E8, (M, K), "a_q", dev)
     _arg(a_scale, _F32, (nb, M), "a_scale", dev)
     return a_q, a_scale
@@ -613,12 +639,6 @@ def _e4m3_out(M, K, dev, a_q, a_scale):
 
 # what a missing or foreign argument raises in those expressions: the naming checks follow
 _NOT_FITTING = (AttributeError, KeyError, TypeError, ValueError)
-
-
-def _act_out(M, K, dev, act):
-    act = workspace(prepared_activations_bytes(M, K), dev) if act is None else act
-    _arg(act, None, None, "act", dev)
-    return act
 
 
 def rmsnorm_quant(x, weight, eps, residual=None, residual_out=None, a_q=None, a_scale=None, rowsum=None, stream=None):
@@ -639,8 +659,8 @@ def rmsnorm_quant(x, weight, eps, residual=None, residual_out=None, a_q=None, a_
     except _NOT_FITTING:
         fits = False
     if not fits:
-        M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out)
-        a_q, a_scale, rowsum = _int8_out(M, K, dev, a_q, a_scale, rowsum)
+        M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out, stream)
+        a_q, a_scale, rowsum = _int8_out(M, K, dev, a_q, a_scale, rowsum, stream)
         index = dev.index
     rc = (_lib or load()).w4a8_rmsnorm_quant(
         x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), eps, code,
@@ -654,8 +674,8 @@ def rmsnorm_quant(x, weight, eps, residual=None, residual_out=None, a_q=None, a_
 def rmsnorm_prepare(x, weight, eps, residual=None, residual_out=None, act=None, stream=None):
     """w4a8_rmsnorm_prepare: rms_norm(x + residual) * weight as the opaque operand of
     `linear_prepared` and `linear_act`.  Returns (act, x + residual or None)."""
-    M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out)
-    act = _act_out(M, K, dev, act)
+    M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out, stream)
+    act = _buffer(act, prepared_activations_bytes(M, K), dev, stream, "act")
     rc = load().w4a8_rmsnorm_prepare(x.data_ptr(), _adr(residual), weight.data_ptr(), eps, code, _adr(residual_out),
                                      act.data_ptr(), _nbytes(act), M, K, _handle(dev.index, stream))
     _check(rc, "w4a8_rmsnorm_prepare")
@@ -680,8 +700,8 @@ def rmsnorm_quant_fp8(x, weight, eps, residual=None, residual_out=None, a_q=None
     except _NOT_FITTING:
         fits = False
     if not fits:
-        M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out)
-        a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
+        M, K, code, dev, residual_out = _norm_in(x, weight, residual, residual_out, stream)
+        a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale, stream)
         index = dev.index
     rc = (_lib or load()).w4a8_rmsnorm_quant_fp8(
         x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), eps, code,
@@ -695,7 +715,7 @@ def rmsnorm_quant_fp8(x, weight, eps, residual=None, residual_out=None, a_q=None
 def swiglu_quant(gate, up, a_q=None, a_scale=None, rowsum=None, stream=None):
     """w4a8_swiglu_quant: silu(gate) * up as INT8 codes for `linear`.  Returns (a_q, a_scale, rowsum)."""
     M, K, ld, code, dev = _gate_up(gate, up)
-    a_q, a_scale, rowsum = _int8_out(M, K, dev, a_q, a_scale, rowsum)
+    a_q, a_scale, rowsum = _int8_out(M, K, dev, a_q, a_scale, rowsum, stream)
     rc = load().w4a8_swiglu_quant(gate.data_ptr(), up.data_ptr(), ld, code, a_q.data_ptr(), a_scale.data_ptr(),
                                   rowsum.data_ptr(), M, K, _handle(dev.index, stream))
     _check(rc, "w4a8_swiglu_quant")
@@ -706,7 +726,7 @@ def swiglu_prepare(gate, up, act=None, stream=None):
     """w4a8_swiglu_prepare: silu(gate) * up as the opaque operand of `linear_prepared` and
     `linear_act` (returned)."""
     M, K, ld, code, dev = _gate_up(gate, up)
-    act = _act_out(M, K, dev, act)
+    act = _buffer(act, prepared_activations_bytes(M, K), dev, stream, "act")
     rc = load().w4a8_swiglu_prepare(gate.data_ptr(), up.data_ptr(), ld, code, act.data_ptr(), _nbytes(act), M, K,
                                     _handle(dev.index, stream))
     _check(rc, "w4a8_swiglu_prepare")
@@ -729,7 +749,7 @@ def swiglu_quant_fp8(gate, up, a_q=None, a_scale=None, stream=None):
         fits = False
     if not fits:
         M, K, ld, code, dev = _gate_up(gate, up)
-        a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
+        a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale, stream)
         index = dev.index
     rc = (_lib or load()).w4a8_swiglu_quant_fp8(
         gate.data_ptr(), up.data_ptr(), ld, code, a_q.data_ptr(), a_scale.data_ptr(), M, K,
@@ -742,14 +762,14 @@ def swiglu_quant_fp8(gate, up, a_q=None, a_scale=None, stream=None):
 def quant_fp8(x, a_q=None, a_scale=None, stream=None):
     """w4a8_quant_fp8: x as e4m3 codes for `fp8_linear`.  Returns (a_q, a_scale)."""
     M, K, code, dev = _rows_in(x, "x")
-    a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale)
+    a_q, a_scale = _e4m3_out(M, K, dev, a_q, a_scale, stream)
     rc = load().w4a8_quant_fp8(x.data_ptr(), code, a_q.data_ptr(), a_scale.data_ptr(), M, K,
                                _handle(dev.index, stream))
     _check(rc, "w4a8_quant_fp8")
     return a_q, a_scale
 
 
-def _fp8_in(a_q, a_scale, w_q, w_scale, bias, y, out_dtype):
+def _fp8_in(a_q, a_scale, w_q, w_scale, bias, y, out_dtype, stream):
     """The checks of fp8_linear that name the offending argument; y allocated when absent."""
     _want(a_q, torch.float8_e4m3fn, "a_q")
     _want(w_q, torch.float8_e4m3fn, "w_q")
@@ -764,7 +784,7 @@ def _fp8_in(a_q, a_scale, w_q, w_scale, bias, y, out_dtype):
     if a_scale is None or w_scale is None:
         raise TypeError("a_scale and w_scale must be torch.Tensors")
     _arg(bias, torch.float32, (N,), "bias", dev)
-    y, _ = _out(y, (M, N), dev, out_dtype if y is None else y.dtype)
+    y, _ = _out(y, (M, N), dev, out_dtype if y is None else y.dtype, stream)
     return M, N, K, y
 
 
@@ -785,7 +805,7 @@ def fp8_linear(a_q, a_scale, w_q, w_scale, bias=None, y=None, out_dtype=None, st
     except _NOT_FITTING:
         fits = False
     if not fits:
-        M, N, K, y = _fp8_in(a_q, a_scale, w_q, w_scale, bias, y, out_dtype)
+        M, N, K, y = _fp8_in(a_q, a_scale, w_q, w_scale, bias, y, out_dtype, stream)
         index, code = y.get_device(), _OUT_DTYPES[y.dtype]
     rc = (_lib or load()).w4a8_fp8_linear(
         a_q.data_ptr(), a_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(),
@@ -886,14 +906,6 @@ def _cache_arg(cache):
     if cache.index != _current_device():
         raise ValueError(f"cache is on {cache.k.device} but the current CUDA device is {_current_device()} "
                          "(the library runs on the current device)")
-
-
-def _new(shape, dtype, device, stream):
-    """An output allocated here; a block freed while `stream` still works on it goes to no other work before that is done."""
-    t = torch.empty(tuple(shape), dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
 
 
 def _heads_arg(t, name, device, dtype=None, shape=None):
@@ -1181,7 +1193,7 @@ def debug_block_acc(a_q, wq, N, m0=0, m_cnt=None, n0=0, n_cnt=None, ws=None, str
     n_cnt = N - n0 if n_cnt is None else n_cnt
     if not (0 <= m0 and 0 <= m_cnt and m0 + m_cnt <= M and 0 <= n0 and 0 <= n_cnt and n0 + n_cnt <= N):
         raise ValueError(f"window rows [{m0}, {m0}+{m_cnt}) x cols [{n0}, {n0}+{n_cnt}) outside [{M}] x [{N}]")
-    acc = torch.empty((m_cnt, n_cnt, K // 64), dtype=torch.int32, device=a_q.device)
+    acc = _new((m_cnt, n_cnt, K // 64), torch.int32, a_q.device, stream)
     ws = _ws(ws, debug_workspace_bytes(m_cnt, n_cnt, K), a_q.device, stream)
     rc = load().w4a8_debug_block_acc(_ptr(a_q), _ptr(wq), M, N, K, m0, m_cnt, n0, n_cnt, _ptr(acc),
                                      _ptr(ws), _nbytes(ws), _stream(stream))
