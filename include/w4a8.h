@@ -433,7 +433,7 @@ int w4a8_kv_read(const w4a8_kv_cache *cache, const int64_t *slots, int64_t token
  *     scales in fp32; more round keys and values (code * scale), or the values' scales, to 11 bits too.
  *     Off from 64 bits by about 2^-10 of the largest |v| at most, and 2^-11 of a logit's terms, before
  *     the output's own rounding.
- *   - A query with a NaN or an infinity makes its own row of out NaN and no other.
+ *   - A query with a NaN or an infinity makes its own row of out NaN, where it sees a key, and no other.
  *   - Equal calls give equal bits; how keys are split depends on the sizes and bounds given, so a
  *     sequence's bits may depend on the batch it is in.
  *   - An entry outside [0, pages) among those read, a length below 0 or past table_stride * page, or a

@@ -96,3 +96,36 @@ def test_another_streams_outputs_of_the_linears():
         assert kept, name
         for g, t in zip(*((v,) if isinstance(v, torch.Tensor) else v for v in (got, want))):
             assert (g is None and t is None) or torch.equal(g.view(torch.uint8), t.view(torch.uint8)), name
+
+
+FORMS = [(1, 2, [1], 0), (1, 2, [300, 2, 40], 0), (1, 16, [1, 700], 0), (2, 7, [900, 2, 130], 20000), (4, 8, [2500, 700, 4], 20000), (90, 2, [400, 90], 0),
+         (70, 1, [6000], 0), (60, 2, [400, 60], 2 ** 30)]
+
+
+def form(seed, n, G, lens, most, fmt, D=128):
+    """A problem whose bound on the keys, `most`, picks one of the ways that the work is cut."""
+    p = problem(seed, [(n, kv) for kv in lens], 2, G, D, 16, fmt)
+    p["max_kv"] = max(p["max_kv"], most)
+    if 0 < most < 2 ** 20:
+        p["table"] = torch.nn.functional.pad(p["table"], (0, most // 16 - p["table"].shape[1]), value=-7)
+    return p
+
+
+@pytest.mark.parametrize("fmt", [I8, E8])
+@pytest.mark.parametrize("code", [50, -50])
+@pytest.mark.parametrize("n,G,lens,most", FORMS, ids=str)
+def test_an_infinite_query_over_codes_of_one_sign(n, G, lens, most, code, fmt):
+    """All logits are infinite, of one sign: NaN whichever it is, for one visible key and for many; the other rows as
+    they were."""
+    p = form(n, n, G, lens, most, fmt)
+    p["cache"].k[..., 5] = torch.tensor(code, device="cuda").to(fmt)
+    want, allowed = reference(p)
+    hurt = [(0, 1), (p["q"].shape[0] - 1, 0), (n // 2, 2 * G - 1), (p["q"].shape[0] - n, G)]
+    for i, (t, h) in enumerate(hurt):
+        p["q"][t, h, 5] = math.inf if i % 2 else -math.inf
+    out = attend(p)
+    rest = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+    for t, h in hurt:
+        rest[t, h] = False
+        assert out[t, h].isnan().all(), (t, h)
+    near(out[rest], want.to(out.device)[rest], allowed.to(out.device)[rest])

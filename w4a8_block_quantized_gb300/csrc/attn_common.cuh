@@ -103,6 +103,12 @@ __device__ __forceinline__ void exponent_of(float v, int none, float& e, float& 
     inv = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
 }
 
+// What a row of q of largest magnitude `most` is multiplied by, 2^8 over its exponent's power.  NaN for a row with an
+// infinity, whose logits would otherwise all be -inf where the codes it meets are of the other sign, as if it saw nothing.
+__device__ __forceinline__ float query_factor(float most, float inv) {
+    return most == INFINITY ? __int_as_float(0x7fffffff) : inv * 256.0f;
+}
+
 // A run's reference as its join reads it, which passes over runs that saw nothing (-inf): not over one whose weights are NaN.
 __device__ __forceinline__ float held_reference(float m, float l) { return l == l ? m : l; }
 

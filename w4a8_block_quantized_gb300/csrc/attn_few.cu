@@ -120,7 +120,7 @@ struct QueryShare {
         float e, inv;
         exponent_of(most, 0, e, inv);
         // largest magnitude to [2^8, 2^9): fp16 keeps what is 2^-33 of it, and a dot product stays below 2^24
-        const float up = inv * 256.0f;
+        const float up = query_factor(most, inv);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) frag[i] = half_pair(v[2 * i] * up, v[2 * i + 1] * up);
         return e - 8.0f;

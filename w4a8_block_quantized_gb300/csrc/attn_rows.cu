@@ -183,7 +183,7 @@ __device__ __forceinline__ void convert_rows(RowAt&& row_at, uint32_t tiles, flo
     }
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
     exponent_of(most, 0, e, inv);
-    const float up = inv * 256.0f;
+    const float up = query_factor(most, inv);
 #pragma unroll 2
     for (int i = c0; i < c0 + HALF; ++i) {
         const uint32_t at = tile + tile_chunk(r & 127, i);
