@@ -129,3 +129,18 @@ def test_an_infinite_query_over_codes_of_one_sign(n, G, lens, most, code, fmt):
         rest[t, h] = False
         assert out[t, h].isnan().all(), (t, h)
     near(out[rest], want.to(out.device)[rest], allowed.to(out.device)[rest])
+
+
+@pytest.mark.parametrize("n,G,lens,most", FORMS, ids=str)
+def test_logits_below_the_smallest_number(n, G, lens, most):
+    """Scale, queries and keys whose product vanishes in fp32: plain means of what is seen, hidden keys stay hidden."""
+    p = form(n + 2, n, G, lens, most, E8)
+    for scale in (1e-45, 1e-38):
+        want, allowed = reference(p, scale=scale)
+        near(attend(p, scale=scale), want, allowed)
+        want, allowed = reference(p, scale=scale, window=40, sinks=3)
+        near(attend(p, scale=scale, window=40, sinks=3), want, allowed)
+    p["q"] *= 2.0 ** -110
+    p["cache"].k_scale.mul_(2.0 ** -60)
+    want, allowed = reference(p)
+    near(attend(p), want, allowed)

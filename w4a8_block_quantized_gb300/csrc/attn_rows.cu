@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 float ev = info.y, iv = info.z;
                 if constexpr (!AHEAD)
                     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ev), "=f"(iv) : "r"(meta + 2 * kStep * 4) : "memory");
-                const float cj = c * info.x;
+                // not 0, which would make NaN of the -inf of hidden keys (a NaN stays one)
+                const float cj = c * info.x < 0x1p-126f ? 0x1p-126f : c * info.x;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tmem_wait_ld32(x[i]);
                 if constexpr (!AHEAD) {
