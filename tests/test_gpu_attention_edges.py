@@ -144,3 +144,23 @@ def test_logits_below_the_smallest_number(n, G, lens, most):
     p["cache"].k_scale.mul_(2.0 ** -60)
     want, allowed = reference(p)
     near(attend(p), want, allowed)
+
+
+@pytest.mark.parametrize("q_dt", [BF, F32])
+@pytest.mark.parametrize("n,G,lens,most", FORMS, ids=str)
+def test_queries_at_the_ends_of_their_type(n, G, lens, most, q_dt):
+    """Rows of every magnitude that the type has, down to its smallest normal numbers and up to its largest."""
+    p = form(n + 1, n, G, lens, most, I8)
+    q = p["q"] = p["q"].to(q_dt)
+    for i, e in enumerate((-126, -124, -121, -120, -119, -100, 100, 126)):
+        t, h = i * (q.shape[0] - 1) // 7, i % q.shape[1]
+        q[t, h] = (q[t, h].float().clamp(-1.9, 1.9) * 2.0 ** e).to(q_dt)
+    q[-1, -1] = torch.finfo(q_dt).max
+    q[0, 0, ::2] = -torch.finfo(q_dt).max
+    scale = 2.0 ** -126
+    want, allowed = reference(p, scale=scale)
+    near(attend(p, scale=scale), want, allowed)
+    q[-1, -1], q[0, 0] = 2.0 ** -126, 2.0 ** -125
+    p["q"] = torch.where(q.float().abs() > 2.0 ** 20, 0.0, q.float()).to(q_dt)
+    want, allowed = reference(p)
+    near(attend(p), want, allowed)

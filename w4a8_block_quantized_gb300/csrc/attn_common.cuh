@@ -103,10 +103,15 @@ __device__ __forceinline__ void exponent_of(float v, int none, float& e, float& 
     inv = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
 }
 
-// What a row of q of largest magnitude `most` is multiplied by, 2^8 over its exponent's power.  NaN for a row with an
-// infinity, whose logits would otherwise all be -inf where the codes it meets are of the other sign, as if it saw nothing.
-__device__ __forceinline__ float query_factor(float most, float inv) {
-    return most == INFINITY ? __int_as_float(0x7fffffff) : inv * 256.0f;
+// A row of q, of largest magnitude `most`, is multiplied by `up`, a power of two, and its logits by 2^e: the largest magnitude
+// comes to [2^8, 2^9), where fp16 keeps what is 2^-33 of it and a dot product stays below 2^24.  Exponents are held to
+// -119 .. 126, where `up` and its inverse's power are numbers: below, rows come to less than 2^8, at 2^127 to less than 2^10.  `up`
+// is NaN for a row with an infinity, whose logits would otherwise all be -inf where the codes it meets are of the other sign,
+// as if it saw nothing.
+__device__ __forceinline__ void query_factor(float most, float& e, float& up) {
+    const int ex = min(max(static_cast<int>(__float_as_uint(most) >> 23), 8), 253);
+    e = static_cast<float>(ex - 127 - 8);
+    up = most == INFINITY ? __int_as_float(0x7fffffff) : __uint_as_float(static_cast<uint32_t>(254 + 8 - ex) << 23);
 }
 
 // A run's reference as its join reads it, which passes over runs that saw nothing (-inf): not over one whose weights are NaN.

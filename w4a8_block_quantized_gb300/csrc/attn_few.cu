@@ -117,13 +117,11 @@ struct QueryShare {
         for (int i = 0; i < N; ++i) most = fmaxf(most, fabsf(v[i]));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        float e, inv;
-        exponent_of(most, 0, e, inv);
-        // largest magnitude to [2^8, 2^9): fp16 keeps what is 2^-33 of it, and a dot product stays below 2^24
-        const float up = query_factor(most, inv);
+        float e, up;
+        query_factor(most, e, up);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) frag[i] = half_pair(v[2 * i] * up, v[2 * i + 1] * up);
-        return e - 8.0f;
+        return e;
     }
 };
 

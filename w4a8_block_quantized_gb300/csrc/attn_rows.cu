@@ -166,7 +166,7 @@ __device__ __forceinline__ void convert_rows(RowAt&& row_at, uint32_t tiles, flo
     const uint32_t tile = tiles + (r >> 7) * (256 * D);
     const float4* row = BF16 ? nullptr : reinterpret_cast<const float4*>(row_at(r));
     const float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float most = 0.0f, e, inv;
+    float most = 0.0f, e, up;
 #pragma unroll 4
     for (int i = c0; i < c0 + HALF; ++i) {
         if constexpr (BF16) {
@@ -182,8 +182,7 @@ __device__ __forceinline__ void convert_rows(RowAt&& row_at, uint32_t tiles, flo
         }
     }
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    exponent_of(most, 0, e, inv);
-    const float up = query_factor(most, inv);
+    query_factor(most, e, up);
 #pragma unroll 2
     for (int i = c0; i < c0 + HALF; ++i) {
         const uint32_t at = tile + tile_chunk(r & 127, i);
@@ -199,7 +198,7 @@ __device__ __forceinline__ void convert_rows(RowAt&& row_at, uint32_t tiles, flo
             sts128(at, half_pair(x.x * up, x.y * up), half_pair(x.z * up, x.w * up), half_pair(y.x * up, y.y * up), half_pair(y.z * up, y.w * up));
         }
     }
-    if ((lane & 1) == 0) exponent[r] = e - 8.0f;
+    if ((lane & 1) == 0) exponent[r] = e;
     fence_proxy_async_smem();
 }
 
