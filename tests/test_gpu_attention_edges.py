@@ -164,3 +164,28 @@ def test_queries_at_the_ends_of_their_type(n, G, lens, most, q_dt):
     p["q"] = torch.where(q.float().abs() > 2.0 ** 20, 0.0, q.float()).to(q_dt)
     want, allowed = reference(p)
     near(attend(p), want, allowed)
+
+
+@pytest.mark.parametrize("fmt", [I8, E8])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("n,G,lens,most", FORMS, ids=str)
+def test_a_key_or_value_that_is_no_number(n, G, lens, most, which, fmt):
+    """A place whose scale is NaN: the rows that see it are NaN, no other is touched."""
+    for window in (dict(), dict(window=50, sinks=3)):
+        p = form(n + 3, n, G, lens, most, fmt)
+        c = p["cache"]
+        want, allowed = reference(p, **window)
+        hurt = torch.zeros(p["q"].shape[:2], dtype=torch.bool, device="cuda")
+        for b, kv in enumerate(lens):
+            for j, h in ((max(0, kv - 1 - n // 2), 0), (max(0, kv - 60), 1)):
+                page = int(p["table"][b, j // 16])
+                (c.k_scale if which == "k" else c.v_scale)[page, h, j % 16] = math.nan
+                (c.k if which == "k" else c.v).view(torch.uint8)[page, h, j % 16] = 0
+                for i in range(n):
+                    at = kv - n + i
+                    if j <= at and (not window or j > at - 50 or j < 3):
+                        hurt[b * n + i, h * G:(h + 1) * G] = True
+        out = attend(p, **window)
+        assert out[hurt].isnan().all()
+        rest = ~hurt
+        near(out[rest], want.to(out.device)[rest], allowed.to(out.device)[rest])

@@ -95,6 +95,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// The larger, or NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
+constexpr uint32_t kBitsInf = 0x7f800000u;  // bits of a number >= 0 from here on: infinity, NaN
+__device__ __forceinline__ float not_a_number() { return __int_as_float(0x7fffffff); }
+
 // The exponent e of v >= 0, and 2^-e; `none` where v has none (0, or past the normal numbers).
 __device__ __forceinline__ void exponent_of(float v, int none, float& e, float& inv) {
     int ex = static_cast<int>(__float_as_uint(v) >> 23);
@@ -111,7 +121,7 @@ __device__ __forceinline__ void exponent_of(float v, int none, float& e, float& 
 __device__ __forceinline__ void query_factor(float most, float& e, float& up) {
     const int ex = min(max(static_cast<int>(__float_as_uint(most) >> 23), 8), 253);
     e = static_cast<float>(ex - 127 - 8);
-    up = most == INFINITY ? __int_as_float(0x7fffffff) : __uint_as_float(static_cast<uint32_t>(254 + 8 - ex) << 23);
+    up = most == INFINITY ? not_a_number() : __uint_as_float(static_cast<uint32_t>(254 + 8 - ex) << 23);
 }
 
 // A run's reference as its join reads it, which passes over runs that saw nothing (-inf): not over one whose weights are NaN.

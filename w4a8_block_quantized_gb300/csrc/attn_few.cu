@@ -563,8 +563,18 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) few_kernel(const __
             }
             // keys whose values are all zero add to l alone: their weights stay small beside other steps'
             float ev, iv;
-            exponent_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]))))),
-                        -24, ev, iv);
+            uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(max_nan(max_nan(vs[0], vs[1]), max_nan(vs[2], vs[3]))));
+            if (most >= kBitsInf) {
+                // a value that is no number: its key's logits are NaN, for the rows that see it, and it meets no weight of 0
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (finite(vs[k])) continue;
+                    ks[k] = not_a_number();
+                    vs[k] = 0.0f;
+                }
+                most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]))));
+            }
+            exponent_of(__uint_as_float(most), -24, ev, iv);
             uint32_t wf[NT][2][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {

@@ -375,8 +375,16 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         float ks = 0.0f, vs = 0.0f;
         auto scales = [&](int j0) {
             ks = vs = 0.0f;
-            if (tid < 128 && some_see(p, p_min, p_max, j0 + tid)) ks = __ldg(p.k_scale + cache_row(p, b, kvh, j0 + tid));
-            if (tid >= kVs && some_see(p, p_min, p_max, j0 + tid - kVs)) vs = __ldg(p.v_scale + cache_row(p, b, kvh, j0 + tid - kVs));
+            // a key or value that is no number makes its key's logits NaN, for the rows that see it, and meets no weight of 0
+            if (tid < 128 && some_see(p, p_min, p_max, j0 + tid)) {
+                const int at = cache_row(p, b, kvh, j0 + tid);
+                ks = __ldg(p.k_scale + at);
+                if (!finite(__ldg(p.v_scale + at))) ks = not_a_number();
+            }
+            if (tid >= kVs && some_see(p, p_min, p_max, j0 + tid - kVs)) {
+                vs = __ldg(p.v_scale + cache_row(p, b, kvh, j0 + tid - kVs));
+                if (!finite(vs)) vs = 0.0f;
+            }
         };
         int j0 = keys.first(s0);
         x.look_up(j0);
@@ -728,7 +736,7 @@ __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ Att
                                     : make_uint4(0, 0, 0, 0);
     const float sc = seen ? __ldg((which ? p.v_scale : p.k_scale) + row_in(p, my_page, kvh, j0 + key)) : 0.0f;
     scale[which][key] = sc;
-    const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(sc));
+    const uint32_t big = __reduce_max_sync(0xffffffffu, finite(sc) ? __float_as_uint(sc) : 0u);
     if ((tid & 31) == 0) most[which][(tid >> 5) & 3] = big;
     __syncthreads();
     const int64_t out = (static_cast<int64_t>(b) * p.heads + kvh) * p.step_cap + step;
@@ -743,7 +751,9 @@ __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ Att
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int r = r0 + i * RS;
-            const float f = scale[w][r] * inv[w];
+            // a key or value that is no number makes its key's logits NaN, for the rows that see it, and meets no weight of 0
+            const float f = w ? (finite(scale[1][r]) ? scale[1][r] * inv[1] : 0.0f)
+                              : (finite(scale[1][r]) ? scale[0][r] * inv[0] : not_a_number());
             const uint32_t u[4] = {raw[w][i].x, raw[w][i].y, raw[w][i].z, raw[w][i].w};
             uint32_t h[8];
 #pragma unroll
