@@ -372,7 +372,8 @@ int w4a8_rope(const void *x, int64_t x_token, int64_t x_head, void *out, int64_t
  * [pages][heads][page], one for a token's head; the stored value is code * scale:
  *   W4A8_KV_INT8  s = max|t| / 127, code = clamp(round_half_away(t / s), +-127)
  *   W4A8_KV_E4M3  s = max|t| / 448, code = e4m3(t * (448 / max|t|)), to nearest even
- * and codes and scale 0 where max|t| < 2^-100.  head_dim 64 or 128; page a power of two from 16 to
+ * and codes and scale 0 where max|t| < 2^-100; codes 0 and scale NaN for a row with a NaN or an infinity (the stored
+ * values are NaN, all of them).  head_dim 64 or 128; page a power of two from 16 to
  * 1024; pages * heads * page < 2^31 (W4A8_ERR_SHAPE).  Scales that attention reads are finite and >= 0, or NaN,
  * with codes that are numbers: a key or value that is none, which makes the rows of out that see it NaN, and no other.
  * 16-byte alignment: all four arrays. */

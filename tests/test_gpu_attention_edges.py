@@ -189,3 +189,29 @@ def test_a_key_or_value_that_is_no_number(n, G, lens, most, which, fmt):
         assert out[hurt].isnan().all()
         rest = ~hurt
         near(out[rest], want.to(out.device)[rest], allowed.to(out.device)[rest])
+
+
+@pytest.mark.parametrize("fmt", [I8, E8])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf], ids=str)
+@pytest.mark.parametrize("D,rot", [(128, 0), (64, 32)])
+def test_rows_that_are_no_numbers_in_the_cache(D, rot, bad, dt, fmt):
+    """A key's or value's row with an element that is no finite number is kept as such: scale NaN, codes 0, read back as
+    NaN; the others are stored as ever."""
+    T, KV = 37, 3
+    cache = B().KVCache.empty(4, KV, 16, D, fmt)
+    k, v = normal(1, T, KV, D).to(dt), normal(2, T, KV, D).to(dt)
+    slots = torch.arange(T, device="cuda")
+    turn = (slots.int(), B().rope_table(rot)) if rot else ()
+    B().kv_write(cache, k, v, slots, *turn)
+    good, held = B().kv_read(cache, slots), [t.clone() for t in (cache.k.view(torch.uint8), cache.v.view(torch.uint8))]
+    broken = [torch.zeros((T, KV), dtype=torch.bool, device="cuda") for _ in "kv"]
+    for i, (t, h, d) in enumerate(((0, 0, 0), (5, 2, D - 1), (T - 1, 1, 17), (20, 0, rot // 2))):
+        (k, v)[i % 2][t, h, d] = bad
+        broken[i % 2][t, h] = True
+    v[9, 1], broken[1][9, 1] = bad, True
+    B().kv_write(cache, k, v, slots, *turn)
+    for got, was, mask, codes, before, scale in zip(B().kv_read(cache, slots), good, broken, (cache.k, cache.v), held, (cache.k_scale, cache.v_scale)):
+        assert got[mask].isnan().all() and torch.equal(got[~mask], was[~mask])
+        assert not R.rows(codes.view(torch.uint8), slots, 16)[mask].any() and R.rows(scale, slots, 16)[mask].isnan().all()
+        assert torch.equal(R.rows(codes.view(torch.uint8), slots, 16)[~mask], R.rows(before, slots, 16)[~mask])

@@ -95,12 +95,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// The larger, or NaN where either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
 constexpr uint32_t kBitsInf = 0x7f800000u;  // bits of a number >= 0 from here on: infinity, NaN
 __device__ __forceinline__ float not_a_number() { return __int_as_float(0x7fffffff); }

@@ -20,6 +20,7 @@
 // block working through tokens with the next one's loads ahead (the write 64 us, at 80 registers a thread for 64).
 #include "attn_internal.h"
 #include "quant_math.cuh"
+#include "sm103_ptx.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -123,17 +124,17 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     return d;
 }
 
-// The codes of 16 values of a row whose largest magnitude over its threads is `amax`; all lanes of a warp.
+// The codes of 16 values of a row whose largest magnitude over its threads is `amax`, NaN if one is; all lanes of a warp.
+// A row with an element that is no finite number has none that its codes could hold: codes 0 and scale NaN.
 __device__ __forceinline__ void codes16(const float (&x)[16], float amax, int format, uint32_t (&code)[4], float& scale) {
-    const bool live = amax >= 0x1p-100f;
-    scale = 0.0f;
+    const bool live = amax >= 0x1p-100f && amax < INFINITY;
+    scale = amax < INFINITY ? 0.0f : __int_as_float(0x7fffffff);
     if (format == W4A8_KV_E4M3) {
         if (live) scale = __fdiv_rn(amax, 448.0f);
         const float inv = live ? __fdiv_rn(448.0f, amax) : 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            code[i] = e4m3_pair(x[4 * i] * inv, x[4 * i + 1] * inv) |
-                      e4m3_pair(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16;
+            code[i] = live ? e4m3_pair(x[4 * i] * inv, x[4 * i + 1] * inv) | e4m3_pair(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16 : 0u;
         return;
     }
     if (live) scale = __fdiv_rn(amax, 127.0f);
@@ -241,8 +242,8 @@ __global__ void __launch_bounds__(kMostThreads, BF16 ? 4 : 3) rotary_kernel(cons
             if (!__any_sync(0xffffffffu, on && kind != 0)) continue;  // a warp of queries
             float amax = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
-            for (int d = p.per_head >> 1; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+            for (int e = 0; e < 16; ++e) amax = max_nan(amax, fabsf(x[e]));
+            for (int d = p.per_head >> 1; d > 0; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
             uint32_t code[4];
             float scale;
             codes16(x, amax, a.cache.format, code, scale);
