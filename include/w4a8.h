@@ -443,7 +443,10 @@ int w4a8_kv_read(const w4a8_kv_cache *cache, const int64_t *slots, int64_t token
  *   - workspace: at least w4a8_attention_workspace_bytes(cache, a) bytes, 16-byte aligned (0: NULL will do), which reads
  *     the sizes, bounds and `total` of `a` but no pointer.  More than 32 rows take 4 bytes for every cached value within
  *     the bounds (max_kv, or the window), as long as that is at most 8 GB; past it the codes are expanded on the way,
- *     which is slower.  The workspace belongs to the call until it is
+ *     which is slower.  A smaller call may
+ *     need more than a larger one (short keys need none, and neither does what is past the 8 GB): ask for each call's
+ *     size, or once for w4a8_attention_workspace_bound, which suffices for every call whose batch, total, max_q and max_kv
+ *     are at most those of `a`, everything else as there.  The workspace belongs to the call until it is
  *     done: calls that may run at the same time (two streams, two graphs) need one each. */
 typedef struct w4a8_attention_args {
     const void *q;
@@ -457,6 +460,7 @@ typedef struct w4a8_attention_args {
     float scale;
 } w4a8_attention_args;
 size_t w4a8_attention_workspace_bytes(const w4a8_kv_cache *cache, const w4a8_attention_args *a);
+size_t w4a8_attention_workspace_bound(const w4a8_kv_cache *cache, const w4a8_attention_args *a);
 int w4a8_attention(const w4a8_kv_cache *cache, const w4a8_attention_args *a, void *workspace,
                    size_t workspace_bytes, void *stream);
 

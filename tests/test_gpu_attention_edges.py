@@ -215,3 +215,19 @@ def test_rows_that_are_no_numbers_in_the_cache(D, rot, bad, dt, fmt):
         assert got[mask].isnan().all() and torch.equal(got[~mask], was[~mask])
         assert not R.rows(codes.view(torch.uint8), slots, 16)[mask].any() and R.rows(scale, slots, 16)[mask].isnan().all()
         assert torch.equal(R.rows(codes.view(torch.uint8), slots, 16)[~mask], R.rows(before, slots, 16)[~mask])
+
+
+def test_one_workspace_for_every_smaller_call():
+    """Sized once for the largest step, it serves the smaller ones, whichever way they are cut."""
+    most = dict(batch=4, total=900, max_q=300, max_kv=20000)
+    ws = None
+    for lens, kv in (([(300, 700)] * 3, 700), ([(1, 300)] * 4, 512), ([(1, 3000)] * 3, 20000), ([(5, 900), (2, 40)], 20000), ([(130, 4000)], 4096)):
+        p = problem(len(lens), lens, 2, 4, 128, 32, I8)
+        p["max_kv"] = max(p["max_kv"], kv)
+        p["table"] = torch.nn.functional.pad(p["table"], (0, 640 - p["table"].shape[1]), value=-7)
+        if ws is None:
+            ws = B().workspace(B().attention_workspace_bound(p["cache"], 8, **most), "cuda")
+        ws.fill_(0xFF)
+        assert B().attention_workspace_bytes(p["q"], p["cache"], len(lens), p["max_q"], p["max_kv"]) <= ws.numel()
+        want, allowed = reference(p)
+        near(attend(p, ws=ws), want, allowed)

@@ -78,6 +78,7 @@ SIGNATURES = {
     "w4a8_kv_write": (ctypes.c_int, [_P, _P, _P]),
     "w4a8_kv_read": (ctypes.c_int, [_P, _P, _I64, _P, _P, ctypes.c_int, _P]),
     "w4a8_attention_workspace_bytes": (_SZ, [_P, _P]),
+    "w4a8_attention_workspace_bound": (_SZ, [_P, _P]),
     "w4a8_attention": (ctypes.c_int, [_P, _P, _P, _SZ, _P]),
     "w4a8_tape_begin": (ctypes.c_int, [_P]),
     "w4a8_tape_end": (ctypes.c_int, [_P, ctypes.POINTER(_P)]),
@@ -1106,12 +1107,23 @@ def kv_read(cache, slots, dtype=None, k=None, v=None, stream=None):
     return k, v
 
 
-def attention_workspace_bytes(q, cache, batch, max_q=1, max_kv=None, window=0, sinks=0):
-    """w4a8_attention_workspace_bytes for an `attention` call with q [total, heads, head_dim] over `cache`."""
-    max_kv = cache.pages * cache.page if max_kv is None else max_kv
+def attention_workspace_bytes(q, cache, batch, max_q=1, max_kv=None, window=0, sinks=0, page_table=None):
+    """w4a8_attention_workspace_bytes for an `attention` call with q [total, heads, head_dim] over `cache`; max_kv absent: what
+    `page_table` holds, as in the call.  A smaller call may need more than a larger one: see attention_workspace_bound."""
+    if max_kv is None:
+        if page_table is None:
+            raise ValueError("max_kv or the call's page_table is needed: the size goes by the bound on the keys")
+        max_kv = page_table.shape[1] * cache.page
     a = _AttentionArgs(total=q.shape[0], batch=batch, q_heads=q.shape[1], max_q=max_q, max_kv=max_kv, window=window,
                        sinks=sinks)
     return int(load().w4a8_attention_workspace_bytes(cache.ref, ctypes.addressof(a)))
+
+
+def attention_workspace_bound(cache, q_heads, batch, total, max_q=1, *, max_kv, window=0, sinks=0):
+    """w4a8_attention_workspace_bound: bytes that suffice for every `attention` call over `cache` with q_heads heads, at most
+    `batch` sequences, `total` rows of q, max_q queries a sequence and max_kv keys, and this window and sinks."""
+    a = _AttentionArgs(total=total, batch=batch, q_heads=q_heads, max_q=max_q, max_kv=max_kv, window=window, sinks=sinks)
+    return int(load().w4a8_attention_workspace_bound(cache.ref, ctypes.addressof(a)))
 
 
 def attention(q, cache, page_table, kv_len, q_start=None, max_q=1, max_kv=None, window=0, sinks=0, scale=None, out=None,
@@ -1120,7 +1132,8 @@ def attention(q, cache, page_table, kv_len, q_start=None, max_q=1, max_kv=None, 
     sliding `window` (0: none) beside which the first `sinks` keys stay visible.  q fp32 or bf16
     [total, heads, head_dim]; page_table int32 [batch, pages of a sequence], kv_len int32 [batch] (the
     queries' own keys included), q_start int32 [batch + 1] with at most max_q queries each, or None: row b
-    is sequence b's one query.  max_kv bounds the lengths (absent: what the page table holds); scale
+    is sequence b's one query.  max_kv bounds the lengths (absent: what the page table holds; where that is much more than
+    the lengths, a bound saves workspace, which for prompts grows with it); scale
     head_dim^-0.5 when absent.  Returns out fp32 or bf16 [total, heads, head_dim] (bf16 when allocated here
     without an out_dtype); its rows that belong to no sequence are left as they are."""
     try:

@@ -201,6 +201,12 @@ size_t w4a8_attention_workspace_bytes(const w4a8_kv_cache* cache, const w4a8_att
     return plan_attention(*cache, *a).bytes;
 }
 
+size_t w4a8_attention_workspace_bound(const w4a8_kv_cache* cache, const w4a8_attention_args* a) {
+    if (check_attention(cache, a) != W4A8_OK) return static_cast<size_t>(-1);
+    if (a->batch == 0 || a->total == 0 || a->max_q == 0) return 0;
+    return bound_attention(*cache, *a);
+}
+
 int w4a8_attention(const w4a8_kv_cache* cache, const w4a8_attention_args* a, void* workspace, size_t workspace_bytes,
                    void* stream) {
     int rc = check_attention(cache, a);

@@ -51,6 +51,8 @@ struct AttnPlan {
 constexpr int kRowTile = 256;  // rows of a CTA of the form for many rows
 
 AttnPlan plan_attention(const w4a8_kv_cache& c, const w4a8_attention_args& a);
+// What suffices for every call within the bounds of `a`.
+size_t bound_attention(const w4a8_kv_cache& c, const w4a8_attention_args& a);
 cudaError_t launch_attention(const w4a8_kv_cache& c, const w4a8_attention_args& a, const AttnPlan& p, void* ws,
                              uint32_t* status, cudaStream_t s);
 

@@ -188,13 +188,36 @@ bool make_rows_map(CUtensorMap* map, const void* p, int64_t rows, int row_bytes,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+namespace {
+
+int rows_of_form(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : kRowTile; }
+// Keys that a sequence's rows see, as bounded.
+int64_t most_seen(const w4a8_attention_args& a, int64_t max_q) {
+    return a.window > 0 ? std::min(a.max_kv, a.window + max_q + a.sinks) : a.max_kv;
+}
+// Few rows: CTAs that fit on the SMs; what they leave to join.
+int64_t few_places(int rows) { return (rows <= 16 ? 3 : 2) * kPlanSms; }
+size_t few_bytes(int64_t ctas, int rows, int64_t dim) {
+    return ctas > 1 ? static_cast<size_t>(ctas) * 2 * rows * (dim + 2) * sizeof(float) + (2 * ctas + 1) * sizeof(int4) : 0;
+}
+// Many rows: what `runs` CTAs leave to join; steps of 128 keys of a sequence, expanded; their bytes and the most of them.
+size_t run_bytes(int64_t runs, int64_t dim) { return static_cast<size_t>(runs) * kRowTile * (dim + 2) * sizeof(float); }
+int64_t steps_of(const w4a8_attention_args& a, int64_t max_q) {
+    const int64_t cap = (a.max_kv + 127) / 128;
+    return a.window > 0 ? std::min(cap, (a.window + max_q + 126) / 128 + 1 + (a.sinks + 127) / 128) : cap;
+}
+int64_t step_bytes(int64_t dim) { return 128 * dim * 2 * 2 + static_cast<int64_t>(sizeof(float4)); }
+constexpr int64_t kMostExpanded = 8LL << 30;
+
+}  // namespace
+
 AttnPlan plan_attention(const w4a8_kv_cache& c, const w4a8_attention_args& a) {
     AttnPlan p;
     const int64_t max_q = std::min(a.max_q, a.total);
     const int64_t rows = max_q * (a.q_heads / c.heads);
-    p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : kRowTile;
+    p.rows = rows_of_form(rows);
     p.row_tiles = static_cast<int>((rows + p.rows - 1) / p.rows);
-    const int64_t seen = a.window > 0 ? std::min(a.max_kv, a.window + max_q + a.sinks) : a.max_kv;
+    const int64_t seen = most_seen(a, max_q);
     const int64_t ctas = a.batch * c.heads * p.row_tiles;
     if (p.rows < kRowTile) {
         // Short keys: a cluster of up to eight CTAs for each sequence and head (item), which joins its sums itself: one launch.
@@ -204,7 +227,7 @@ AttnPlan plan_attention(const w4a8_kv_cache& c, const w4a8_attention_args& a) {
         // keys 30.5 and 31.3, 45 and 46.
         // Otherwise as many CTAs as fit on the SMs share the keys of all items; below 128 keys each, fewer of them.
         const int64_t item = std::max<int64_t>(1, (seen + 127) / 128), units = ctas * item;
-        const int64_t places = (p.rows <= 16 ? 3 : 2) * kPlanSms;
+        const int64_t places = few_places(p.rows);
         int cluster = 1;
         while (cluster < 8 && 2 * cluster <= item && 2 * cluster * ctas <= 2 * kPlanSms) cluster *= 2;
         int64_t each = (item + cluster - 1) / cluster;
@@ -225,29 +248,38 @@ AttnPlan plan_attention(const w4a8_kv_cache& c, const w4a8_attention_args& a) {
             return p;
         }
         p.splits = static_cast<int>(std::min<int64_t>(places, units));
-        if (p.splits > 1)
-            p.bytes = static_cast<size_t>(p.splits) * 2 * p.rows * (c.head_dim + 2) * sizeof(float) + (2 * p.splits + 1) * sizeof(int4);
+        p.bytes = few_bytes(p.splits, p.rows, c.head_dim);
         return p;
     }
     // One CTA an SM: as many runs of an item's keys as fill the SMs, of at least four steps of 128 keys each.  Up to eight steps
     // in one run (64 rows of 32 heads, 1024 keys: one run 22.7 us, two 24.3; 2048 keys: two runs 29.9, four 25.8).
     p.splits = static_cast<int>(std::min<int64_t>({std::max<int64_t>(1, kPlanSms / ctas), seen <= 1024 ? 1 : (seen + 511) / 512, 256}));
-    if (p.splits > 1) p.bytes = static_cast<size_t>(ctas) * p.splits * p.rows * (c.head_dim + 2) * sizeof(float);
+    if (p.splits > 1) p.bytes = run_bytes(ctas * p.splits, c.head_dim);
     // Keys and values expanded once, ahead, unless that takes more than 8 GB of workspace.  Measured, ahead and inside: prompts
     // of 128, 512 and 2048 tokens 12.3 and 13.8 us, 16.7 and 22.9, 48 and 75; 16 prompts of 512 tokens 67 and 88; 64 tokens
     // over 2048 keys 25.8 and 31.1; 32 sequences of 16 tokens over 4096 keys 169 and 173.
-    int64_t cap = (a.max_kv + 127) / 128;
-    if (a.window > 0) cap = std::min(cap, (a.window + max_q + 126) / 128 + 1 + (a.sinks + 127) / 128);
-    const int64_t steps = a.batch * c.heads * cap;
-    if (cap > 0 && steps <= (1LL << 23)) {
-        const int64_t bytes = steps * (128 * c.head_dim * 2 * 2 + static_cast<int64_t>(sizeof(float4)));
-        if (bytes <= (8LL << 30)) {
-            p.step_cap = static_cast<int>(cap);
-            p.expand_at = (p.bytes + 1023) & ~static_cast<size_t>(1023);
-            p.bytes = p.expand_at + static_cast<size_t>(bytes);
-        }
+    const int64_t cap = steps_of(a, max_q), steps = a.batch * c.heads * cap;
+    if (cap > 0 && steps <= kMostExpanded / step_bytes(c.head_dim)) {
+        p.step_cap = static_cast<int>(cap);
+        p.expand_at = (p.bytes + 1023) & ~static_cast<size_t>(1023);
+        p.bytes = p.expand_at + static_cast<size_t>(steps * step_bytes(c.head_dim));
     }
     return p;
+}
+
+size_t bound_attention(const w4a8_kv_cache& c, const w4a8_attention_args& a) {
+    const int64_t max_q = std::min(a.max_q, a.total), group = a.q_heads / c.heads, rows = max_q * group;
+    const int64_t seen = most_seen(a, max_q), items = a.batch * c.heads, units = items * std::max<int64_t>(1, (seen + 127) / 128);
+    size_t most = 0;
+    for (int r = rows_of_form(group); r <= 32 && r <= rows_of_form(rows); r *= 2)
+        most = std::max(most, few_bytes(std::min(few_places(r), units), r, c.head_dim));
+    if (rows > 32) {
+        // more than one run an item only where all runs fit the SMs; the expansion begins on a whole 1024 bytes
+        const size_t runs = seen > 1024 ? run_bytes(kPlanSms, c.head_dim) : 0;
+        const int64_t steps = std::min(items * steps_of(a, max_q), kMostExpanded / step_bytes(c.head_dim));
+        most = std::max(most, runs + 1023 + static_cast<size_t>(steps * step_bytes(c.head_dim)));
+    }
+    return most;
 }
 
 cudaError_t launch_attention(const w4a8_kv_cache& c, const w4a8_attention_args& a, const AttnPlan& plan, void* ws,
