@@ -958,18 +958,17 @@ def _apart(a, b, name, in_place=True):
         return
     ends = [t.data_ptr() + t.element_size() * (1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride())))
             for t in (a, b)]
-    if a.numel() and b.numel() and a.data_ptr() < ends[1] and b.data_ptr() < ends[0] and \
-            a.untyped_storage().data_ptr() == b.untyped_storage().data_ptr() and not _interleaved(a, b):
+    if a.numel() and b.numel() and a.data_ptr() < ends[1] and b.data_ptr() < ends[0] and not _interleaved(a, b):
         raise ValueError(f"{name} overlaps an input of the call")
 
 
 def _interleaved(a, b):
-    """Two slices of one [tokens, width] array, each inside columns of its own."""
-    if a.stride(0) != b.stride(0) or a.shape[0] < 2:
+    """Two slices of one [tokens, width] array, each inside columns of its own; all in bytes: their types may differ."""
+    st = a.stride(0) * a.element_size()
+    if st != b.stride(0) * b.element_size() or a.shape[0] < 2 or st == 0:
         return False
-    el, st = a.element_size(), a.stride(0)
-    width = [1 + sum((n - 1) * s for n, s in zip(t.shape[1:], t.stride()[1:])) for t in (a, b)]
-    gap = (b.data_ptr() - a.data_ptr()) // el % st
+    width = [t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape[1:], t.stride()[1:]))) for t in (a, b)]
+    gap = (b.data_ptr() - a.data_ptr()) % st
     return width[0] <= gap and gap + width[1] <= st
 
 
