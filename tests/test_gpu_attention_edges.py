@@ -231,3 +231,29 @@ def test_one_workspace_for_every_smaller_call():
         assert B().attention_workspace_bytes(p["q"], p["cache"], len(lens), p["max_q"], p["max_kv"]) <= ws.numel()
         want, allowed = reference(p)
         near(attend(p, ws=ws), want, allowed)
+
+
+def test_a_tape_holds_what_its_calls_allocated():
+    """Outputs and workspaces that recorded calls made for themselves live as long as the tape: later allocations get other
+    memory, and a replay writes none that is theirs."""
+    p = problem(5, [(1, 3000)] * 3, 2, 4, 128, 32, I8)
+    p["max_kv"] = 20000
+    p["table"] = torch.nn.functional.pad(p["table"], (0, 20000 // 32 - p["table"].shape[1]), value=-7)
+    need = B().attention_workspace_bytes(p["q"], p["cache"], 3, p["max_q"], p["max_kv"])
+    assert need > 1 << 20
+    want = attend(p)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        warm = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)] + [torch.empty_like(want) for _ in range(2)]
+        del warm
+        torch.cuda.synchronize()
+        with B().Tape(s) as tape:
+            out = attend(p)
+        others = [torch.full((need,), 0x77, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        out.zero_()
+        for _ in range(3):
+            tape.replay(s)
+        s.synchronize()
+        assert torch.equal(out, want)
+        assert all((t == 0x77).all() for t in others)
+        tape.free()

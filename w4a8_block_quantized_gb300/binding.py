@@ -186,7 +186,20 @@ def _new(shape, dtype, device, stream):
     work queued there uses it goes to no other work before that is done."""
     with _on(stream, device):
         t = torch.empty(tuple(shape), dtype=dtype, device=device)
-    return _returned(t, stream)
+    return _returned(_taped(t, stream), stream)
+
+
+_recording = []  # the tapes that are being recorded
+
+
+def _taped(t, stream):
+    """`t`, held by the tape that records `stream`, if one does: what a recorded call allocates is written by every replay."""
+    if _recording:
+        handle = (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+        for tape in _recording:
+            if tape.recorded == handle:
+                tape.keep.append(t)
+    return t
 
 
 def _returned(t, stream):
@@ -200,7 +213,7 @@ def _ws(ws, need: int, device, stream=None):
     a temporary one, allocated for `stream` and dropped when the call returns."""
     if ws is None:
         with _on(stream, device):
-            return workspace(need, device)
+            return _taped(workspace(need, device), stream)
     _arg(ws, None, None, "ws", device)
     return ws
 
@@ -1225,17 +1238,24 @@ def selftest_wait_timeout(limit_us: int, stream=None) -> None:
 class Tape:
     """A recorded call sequence (w4a8_tape_*): `with Tape(stream) as t:` records the library
     calls made on `stream` inside the block; `t.replay(stream)` runs them again with one
-    launch.  The tensors the recorded calls used must stay alive while the tape is."""
+    launch.  The tensors given to the recorded calls must stay alive while the tape is; outputs and
+    workspaces that the calls allocated for themselves the tape holds.  (Device memory cannot be
+    requested while a stream is recorded: such calls are made once before, so that the allocator has
+    their blocks at hand.)"""
 
     def __init__(self, stream):
         self.stream = stream
         self.handle = None
+        self.recorded, self.keep = None, []
 
     def __enter__(self):
         _check(load().w4a8_tape_begin(_stream(self.stream)), "w4a8_tape_begin")
+        self.recorded = _stream(self.stream).value
+        _recording.append(self)
         return self
 
     def __exit__(self, exc_type, exc, tb):
+        _recording.remove(self)
         h = _P()
         rc = load().w4a8_tape_end(_stream(self.stream), ctypes.byref(h))
         if exc_type is None:
@@ -1248,6 +1268,10 @@ class Tape:
     def replay(self, stream=None):
         if self.handle is None:
             raise RuntimeError("tape not recorded")
+        if self.keep:
+            used = torch.cuda.current_stream() if stream is None else stream
+            for t in self.keep:
+                t.record_stream(used)
         _check(load().w4a8_tape_replay(self.handle, _stream(stream)), "w4a8_tape_replay")
 
     def kernels(self) -> int:
@@ -1260,6 +1284,7 @@ class Tape:
         if self.handle is not None:
             load().w4a8_tape_free(self.handle)
             self.handle = None
+        self.keep.clear()
 
     def __del__(self):
         try:
