@@ -374,8 +374,9 @@ int w4a8_rope(const void *x, int64_t x_token, int64_t x_head, void *out, int64_t
  *   W4A8_KV_E4M3  s = max|t| / 448, code = e4m3(t * (448 / max|t|)), to nearest even
  * and codes and scale 0 where max|t| < 2^-100; codes 0 and scale NaN for a row with a NaN or an infinity (the stored
  * values are NaN, all of them).  head_dim 64 or 128; page a power of two from 16 to
- * 1024; pages * heads * page < 2^31 (W4A8_ERR_SHAPE).  Scales that attention reads are finite and >= 0, or NaN,
- * with codes that are numbers: a key or value that is none, which makes the rows of out that see it NaN, and no other.
+ * 1024; pages * heads * page < 2^31 (W4A8_ERR_SHAPE).  Scales that attention reads are >= 0 and below
+ * 2^127, or NaN, with codes that are numbers: a key or value that is none, which makes the rows of out that see it NaN, and no
+ * other.  The values' scales that a row sees, zeros apart, lie within 2^100 of one another (weights are held beside them).
  * 16-byte alignment: all four arrays. */
 #define W4A8_KV_INT8 0
 #define W4A8_KV_E4M3 1
@@ -415,7 +416,8 @@ int w4a8_kv_read(const w4a8_kv_cache *cache, const int64_t *slots, int64_t token
 
 /* Attention of the newest tokens of each sequence over the cache.
  * Sequence b has kv_len[b] keys (int32 [batch]); key j lies in page page_table[b][j / page] (int32, rows
- * `table_stride` entries apart, which hold kv_len[b] / page, rounded up, entries; the others are not read).
+ * `table_stride` entries apart, which hold kv_len[b] / page, rounded up, entries, all of them pages of the cache: those of keys
+ * that a window hides may be read too; the others are not read).
  * Its queries are the rows q_start[b] .. q_start[b+1] - 1 of q [total][q_heads][head_dim] (int32 [batch + 1],
  * rising), at most max_q of them; q_start NULL: one query each, row b.  The keys of the queries themselves are in the
  * cache already: query i of n has position p = kv_len[b] - n + i and sees
@@ -433,15 +435,16 @@ int w4a8_kv_read(const w4a8_kv_cache *cache, const int64_t *slots, int64_t token
  *     A row of q is first multiplied by a power of two: bf16 queries are then exact, fp32 queries keep 11
  *     bits, and so do probabilities.  Up to 32 rows (max_q * q_heads / heads) take the codes exactly and the
  *     scales in fp32; more round keys and values (code * scale), or the values' scales, to 11 bits too.
- *     Off from 64 bits by about 2^-10 of the largest |v| at most, and 2^-11 of a logit's terms, before
- *     the output's own rounding.
+ *     Off from 64 bits by about 2^-10 of the largest |v| at most, and 2^-11 of a logit's terms (where keys are rounded: of the
+ *     largest logit's among 128 neighbouring keys), before the output's own rounding, for fp32 outputs as well.
  *   - A query with a NaN or an infinity makes its own row of out NaN, where it sees a key, and no other.
  *   - Equal calls give equal bits; how keys are split depends on the sizes and bounds given, so a
  *     sequence's bits may depend on the batch it is in.
  *   - An entry outside [0, pages) among those read, a length below 0 or past table_stride * page, or a
  *     q_start outside [0, total] records W4A8_ERR_INDEX; the sequence's rows are then unspecified.
  *   - workspace: at least w4a8_attention_workspace_bytes(cache, a) bytes, 16-byte aligned (0: NULL will do), which reads
- *     the sizes, bounds and `total` of `a` but no pointer.  More than 32 rows take 4 bytes for every cached value within
+ *     the sizes, bounds and `total` of `a` but no pointer.  More than 32 rows -- one token of a group of more than
+ *     32 heads too -- take 4 bytes for every cached value within
  *     the bounds (max_kv, or the window), as long as that is at most 8 GB; past it the codes are expanded on the way,
  *     which is slower.  A smaller call may
  *     need more than a larger one (short keys need none, and neither does what is past the 8 GB): ask for each call's

@@ -257,3 +257,16 @@ def test_a_tape_holds_what_its_calls_allocated():
         assert torch.equal(out, want)
         assert all((t == 0x77).all() for t in others)
         tape.free()
+
+
+@pytest.mark.parametrize("up", [90, -90])
+@pytest.mark.parametrize("n,G,lens,most", FORMS, ids=str)
+def test_value_scales_far_apart(n, G, lens, most, up):
+    """Keys whose values are 2^90 of the others': the small ones add to the weights' sum all the same."""
+    p = form(n + 4, n, G, lens, most, I8)
+    c = p["cache"]
+    for b, kv in enumerate(lens):
+        for j in range(kv // 2, kv):
+            c.v_scale[int(p["table"][b, j // 16]), :, j % 16] *= 2.0 ** up
+    want, allowed = reference(p)
+    near(attend(p), want, allowed)

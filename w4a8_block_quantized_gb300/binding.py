@@ -3,6 +3,9 @@
 Argument marshalling only: every step of the computation runs in the library's CUDA
 kernels.  PyTorch supplies device memory and the current stream.  There is no CPU
 fallback: if the library is missing or the GPU is not an sm_103 part, calls raise.
+
+A call that names a `stream` runs there: the caller orders it behind what its inputs wait for, and keeps the
+inputs until it is done.  What the call allocates is allocated for that stream.
 """
 from __future__ import annotations
 

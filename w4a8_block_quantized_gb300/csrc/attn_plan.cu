@@ -221,10 +221,11 @@ AttnPlan plan_attention(const w4a8_kv_cache& c, const w4a8_attention_args& a) {
     const int64_t ctas = a.batch * c.heads * p.row_tiles;
     if (p.rows < kRowTile) {
         // Short keys: a cluster of up to eight CTAs for each sequence and head (item), which joins its sums itself: one launch.
-        // Measured, so and dealt out: one sequence, 8 items of 512, 1024, 2048 and 4096 keys 6.5 and 9.1 us, 6.8 and 9.4,
-        // 8.2 and 9.9, 11.1 and 10.6 (but a launch less to issue); 64 items of 512 keys and 32 rows 14.8 and 21.2; 256 items
-        // of up to 512, 1024 and 2048 keys 12.4 and 15.6, 20.2 and 20.7, 34.9 and 28.9; 1024 items of up to 512 and 1024
-        // keys 30.5 and 31.3, 45 and 46.
+        // Measured, so and dealt out: one sequence, 8 items of 512, 1024, 2048 and 4096 keys 6.9 and 9.3 us, 7.2 and 9.8,
+        // 8.7 and 10.3, 11.6 and 10.7 (but a launch less to issue); 32 items of up to 512, 2048 and 4096 keys 7.3 and 12.3,
+        // 10.3 and 13.0, 14.0 and 15.2; 64 items of 512 keys and 32 rows 14.8 and 21.2; 256 items of up to 512, 1024 and 2048
+        // keys 12.7 and 15.9, 20.0 and 18.8, 34.9 and 28.9 (dealt out, by the rule); 512 items of up to 256, 512 and 1024 keys
+        // 14.9 and 14.7, 19.1 and 21.0, 30.8 and 29.3; 1024 items 22.4 and 20.3, 31.6 and 33.9, 44.8 and 44.2.
         // Otherwise as many CTAs as fit on the SMs share the keys of all items; below 128 keys each, fewer of them.
         const int64_t item = std::max<int64_t>(1, (seen + 127) / 128), units = ctas * item;
         const int64_t places = few_places(p.rows);
@@ -235,8 +236,11 @@ AttnPlan plan_attention(const w4a8_kv_cache& c, const w4a8_attention_args& a) {
         bool clustered = ctas <= (1 << 20) && (each <= 4 || (each <= 8 && ctas >= kPlanSms));
         if (!clustered && seen < a.max_kv) {
             // A window, which keeps most sequences' keys equally many: as many CTAs as clusters fill seven eighths of the
-            // SMs' places with (64 items, 33 units: clusters of 6 and 7, 21.4 and 30.6 us).  So and dealt out, of 4096
-            // keys: 64, 128 items 21.4 and 25.1, 31.5 and 37.2; 8 rows, 16 and 32 rows 31.5 and 37.2, 46.9 and 52.9, 43.9 and 60.4.
+            // SMs' places with (64 items, 33 units: clusters of 6 and 7, 21.4 and 30.6 us).  So and dealt out, for windows of
+            // 2048, 4096, 6000 and 8192 keys: 64 items of up to 8 rows 13.5 and 17.2 us, 21.8 and 24.8, 26.1 and 29.6, 32.3 and
+            // 36.0; of 16 rows 21.1 and 24.6, 32.6 and 34.1, 38.8 and 43.3, 47.6 and 52.4; of 32 rows, up to 6000 keys, 28.5 and
+            // 32.1, 42.2 and 44.5, 51.7 and 54.7; 128 items of 8 rows, up to 6000 keys, 21.8 and 27.0, 32.3 and 36.0, 42.6 and
+            // 45.4; of 16 rows 32.5 and 38.7, 47.8 and 52.5, 62.4 and 66.0.
             const int64_t fit = places * 7 / 8;
             cluster = static_cast<int>(std::min<int64_t>(8, fit / ctas));
             each = cluster > 0 ? (item + cluster - 1) / cluster : item;
